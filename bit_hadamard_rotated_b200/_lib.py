@@ -21,6 +21,7 @@ HQ_F16, HQ_BF16, HQ_F32 = 0, 1, 2
 HQ_MOE_POS, HQ_MOE_H, HQ_MOE_D = 0, 1, 2
 HQ_LAYOUT_PACKED, HQ_LAYOUT_BITPLANES = 0, 1
 HQ_PATH_GEMV, HQ_PATH_TENSOR, HQ_PATH_GEMV32 = 0, 1, 2
+HQ_FP4_NV, HQ_FP4_MX = 0, 1
 
 _vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 
@@ -43,6 +44,11 @@ class HqReadout(ctypes.Structure):
 class HqKvCache(ctypes.Structure):
     _fields_ = [("head_dim", _i), ("n_kv_heads", _i), ("capacity", _i), ("k_codes", _vp), ("k_scale", _vp),
                 ("k_min", _vp), ("v_codes", _vp), ("v_scale", _vp), ("v_min", _vp)]
+
+
+class HqFp4Matrix(ctypes.Structure):
+    _fields_ = [("format", _i), ("rows", _i), ("K", _i), ("codes", _vp), ("scales", _vp), ("tensor_scale", _vp),
+                ("n_tensor_scales", _i)]
 
 
 class HqError(RuntimeError):
@@ -120,6 +126,33 @@ def lib() -> ctypes.CDLL:
         L.hq_set_gemv32_min_batch.restype = _i
         L.hq_linear_path.argtypes = [ctypes.POINTER(HqWeight), _i]
         L.hq_linear_path.restype = _i
+        pm = ctypes.POINTER(HqFp4Matrix)
+        L.hq_fp4_scale_bytes.argtypes = [_i, _i, _i]
+        L.hq_fp4_scale_bytes.restype = _sz
+        L.hq_fp4_quantize.argtypes = [_vp, _i, _sz, pm, _vp, _vp]
+        L.hq_fp4_quantize.restype = _i
+        L.hq_fp4_tensor_scale.argtypes = [_vp, _i, _sz, _i, _i, _vp, _vp, _sz, _vp]
+        L.hq_fp4_tensor_scale.restype = _i
+        L.hq_fp4_matmul_workspace_size.argtypes = [pm, _i]
+        L.hq_fp4_matmul_workspace_size.restype = _sz
+        L.hq_fp4_matmul.argtypes = [pm, pm, _vp, _i, _sz, _vp, _sz, _vp]
+        L.hq_fp4_matmul.restype = _i
+        L.hq_fp4_linear_workspace_size.argtypes = [pm, _i]
+        L.hq_fp4_linear_workspace_size.restype = _sz
+        L.hq_fp4_linear.argtypes = [pm, _vp, _i, _sz, _i, _vp, _vp, _i, _sz, _vp, _sz, _vp]
+        L.hq_fp4_linear.restype = _i
+        L.hq_fp4_linear_launches.argtypes = []
+        L.hq_fp4_linear_launches.restype = _i
+        L.hq_moe_sort_workspace_size.argtypes = [_i, _i, _i]
+        L.hq_moe_sort_workspace_size.restype = _sz
+        L.hq_moe_sort.argtypes = [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]
+        L.hq_moe_sort.restype = _i
+        L.hq_moe_gather.argtypes = [_vp, _i, _vp, _i, _i, _i, _vp, _i, _vp]
+        L.hq_moe_gather.restype = _i
+        L.hq_moe_combine.argtypes = [_vp, _i, _i, _vp, _vp, _i, _i, _i, _vp, _i, _vp]
+        L.hq_moe_combine.restype = _i
+        L.hq_moe_combine_grad.argtypes = [_vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp]
+        L.hq_moe_combine_grad.restype = _i
         _lib = L
     return _lib
 

@@ -1,0 +1,350 @@
+// fp4_quant.cu -- rows of real values to microscaled 4-bit floating point:
+// E2M1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign) with one scale per block
+// (16 values and an E4M3 scale, or 32 values and a power-of-two E8M0 scale).
+//
+// A thread takes 16 consecutive values of a row: 16-byte loads, the block's
+// largest magnitude in registers (E8M0 blocks: one shuffle with the next
+// thread), 8 bytes of codes out.  The scales of four neighbouring blocks meet
+// in one word through shuffles, which is the 4-byte cell that the tensor
+// cores' scale tile keeps together (include/hq.h).
+//
+// Bound: HBM.  Each value is read once and leaves as half a byte, a share of a
+// scale and, if asked for, its rounded value.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "fp4.cuh"
+#include "hq_common.cuh"
+#include "hq_internal.h"
+#include "hq_io.cuh"
+#include "hq_launch.cuh"
+
+namespace hq {
+namespace fp4 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The block scale of amax: the scale byte and its value times the tensor
+// scale.  In IEEE single precision, as the header defines it.
+template <int FMT>
+__device__ __forceinline__ void block_scale(float amax, float ts, uint32_t& byte, float& eff) {
+  if constexpr (FMT == HQ_FP4_NV) {
+    byte = __nv_cvt_float_to_fp8(__fdiv_rn(amax, __fmul_rn(6.f, ts)), __NV_SATFINITE, __NV_E4M3);
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3);
+    eff = __fmul_rn(__half2float(__half(h)), ts);
+  } else {
+    // floor(log2 amax) - 2, at least -127: the exponent field of a normal
+    // amax less 2 (a subnormal amax gives the smallest scale either way)
+    const int f = static_cast<int>(__float_as_uint(amax) >> 23) - 2;
+    byte = static_cast<uint32_t>(max(f, 0));
+    eff = byte == 0 ? __uint_as_float(1u << 22) : __uint_as_float(byte << 23);
+  }
+}
+
+// x / eff for 16 values.  Where 1 / eff is far from under- and overflow, by
+// Markstein's quotient correction (IBM J. Res. Dev. 34, 1990): with y the
+// correctly rounded 1 / eff, q = x y is within an ulp and q + (x - q eff) y,
+// both steps fused, rounds to the correctly rounded quotient; so ties between
+// codes are met exactly, at 3 operations a value instead of a division.
+__device__ __forceinline__ void quotients(float (&v)[16], float eff) {
+  if (eff >= 0x1p-100f && eff <= 0x1p100f) {
+    const float y = __frcp_rn(eff);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float q = __fmul_rn(v[i], y);
+      v[i] = __fmaf_rn(__fmaf_rn(-q, eff, v[i]), y, q);
+    }
+  } else if (eff > 0.f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(v[i], eff);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = copysignf(0.f, v[i]);
+  }
+}
+
+// Two values to two E2M1 codes (low nibble first), round to nearest even,
+// saturating.
+__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float2 from_e2m1x2(uint32_t b) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(b));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const float (&v)[16]) {
+  constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < 16 / PER; ++i) {
+    uint4 u;
+    T* t = reinterpret_cast<T*>(&u);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) t[j] = from_f32<T>(v[i * PER + j]);
+    reinterpret_cast<uint4*>(p)[i] = u;
+  }
+}
+
+struct QuantArgs {
+  const void* x;
+  size_t ldx;
+  int rows;       // source rows
+  int rows_pad;   // rows whose scales are written (whole tiles; beyond `rows`: zero)
+  int K;
+  int c_pad;      // 16-value chunks per row of whole scale tiles
+  int lanes_log;  // log2 of the threads along a row
+  const float* ts;
+  uint8_t* codes;
+  uint8_t* scales;
+  int kb;          // scale tiles along K
+  void* values;
+  const int32_t* pos;  // destination rows [rows][k], or nullptr: row r to row r
+  int k;
+  int dst_rows;
+};
+
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lanes = 1 << a.lanes_log;
+  const long row = static_cast<long>(blockIdx.x) * (kThreads >> a.lanes_log) + (threadIdx.x >> a.lanes_log);
+  const int c = blockIdx.y * lanes + (threadIdx.x & (lanes - 1));
+  const bool live = row < a.rows && c * 16 < a.K;
+  float v[16];
+  if (live) {
+    load_chunk<T, 16>(static_cast<const T*>(a.x) + row * a.ldx + c * 16, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  }
+  float amax = 0.f;
+  bool fine = true;  // every value finite
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float m = fabsf(v[i]);
+    amax = fmaxf(amax, m);
+    fine = fine && m < INFINITY;
+  }
+  if constexpr (FMT == HQ_FP4_MX) {
+    amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
+    fine = __shfl_xor_sync(~0u, static_cast<int>(fine), 1) && fine;
+  }
+  const float ts = FMT == HQ_FP4_NV && a.ts != nullptr ? __ldg(a.ts) : 1.f;
+  uint32_t byte;
+  float eff;
+  block_scale<FMT>(amax, ts, byte, eff);
+  if (!fine) {  // the format's NaN as the scale, over codes of zero
+    byte = FMT == HQ_FP4_NV ? 0x7Fu : 0xFFu;
+    eff = __uint_as_float(0x7FC00000u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  } else {
+    quotients(v, eff);
+  }
+  if (!live) byte = 0;
+  uint2 code;
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = to_e2m1x2(v[2 * i], v[2 * i + 1]);
+  code.x = w[0] | w[1] << 8 | w[2] << 16 | w[3] << 24;
+  code.y = w[4] | w[5] << 8 | w[6] << 16 | w[7] << 24;
+  // four blocks' scales in one word
+  constexpr int S = FMT == HQ_FP4_NV ? 0 : 1;  // log2 of the threads per block
+  uint32_t sw = byte << (8 * (c >> S & 3));
+  sw |= __shfl_xor_sync(~0u, sw, 1 << S);
+  sw |= __shfl_xor_sync(~0u, sw, 2 << S);
+  const bool scale_lane = (c & ((4 << S) - 1)) == 0 && c < a.c_pad;
+  const int st = c >> (2 + S);  // scale tile along K
+  if (a.pos == nullptr) {
+    if (live) *reinterpret_cast<uint2*>(a.codes + row * (a.K / 2) + c * 8) = code;
+    if (scale_lane && row < a.rows_pad) *reinterpret_cast<uint32_t*>(a.scales + scale_cell(row, st, a.kb)) = sw;
+    if (a.values != nullptr && live) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = from_e2m1x2(w[i]);
+        v[2 * i] = f.x * eff;
+        v[2 * i + 1] = f.y * eff;
+      }
+      store16<T>(static_cast<T*>(a.values) + row * a.K + c * 16, v);
+    }
+  } else if (row < a.rows) {
+    for (int j = 0; j < a.k; ++j) {
+      const int r = __ldg(a.pos + row * a.k + j);
+      if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.dst_rows)) continue;
+      if (live) *reinterpret_cast<uint2*>(a.codes + static_cast<long>(r) * (a.K / 2) + c * 8) = code;
+      if (scale_lane) *reinterpret_cast<uint32_t*>(a.scales + scale_cell(r, st, a.kb)) = sw;
+    }
+  }
+}
+
+// The largest magnitude of a tensor over 2688 (= 6 * 448, the largest value
+// of a code times the largest block scale), 1 for an all-zero tensor.  Every
+// block folds its maximum into ws[0] (magnitudes order as their bit patterns;
+// a NaN's is above all), the last one writes the result and puts both words
+// back to zero.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) tensor_scale_kernel(const T* __restrict__ x, size_t ldx, int rows,
+                                                                int chunks, float* __restrict__ out,
+                                                                uint32_t* __restrict__ ws) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const size_t total = static_cast<size_t>(rows) * chunks;
+  uint32_t m = 0;
+  for (size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += static_cast<size_t>(gridDim.x) * kThreads) {
+    const size_t r = i / chunks;
+    float v[16];
+    load_chunk<T, 16>(x + r * ldx + (i - r * chunks) * 16, v);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  }
+  m = __reduce_max_sync(~0u, m);
+  __shared__ uint32_t part[kThreads / 32];
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < kThreads / 32; ++i) m = max(m, part[i]);
+    atomicMax(ws, m);
+    __threadfence();
+    if (atomicAdd(ws + 1, 1u) == gridDim.x - 1) {
+      __threadfence();
+      const float s = __fdiv_rn(__uint_as_float(atomicExch(ws, 0u)), 2688.f);
+      *out = s == 0.f ? 1.f : s;
+      ws[1] = 0;
+    }
+  }
+}
+
+template <typename T>
+cudaError_t quantize_launch(int fmt, const QuantArgs& a, dim3 grid, cudaStream_t st) {
+  return fmt == HQ_FP4_NV
+             ? launch_pdl(quantize_rows_kernel<T, HQ_FP4_NV>, grid, dim3(kThreads), 0, st, true, a)
+             : launch_pdl(quantize_rows_kernel<T, HQ_FP4_MX>, grid, dim3(kThreads), 0, st, true, a);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize(int fmt, hq_dtype xd, const void* x, size_t ldx, int rows, int K, const float* ts,
+                            uint8_t* codes, uint8_t* scales, void* values, const int32_t* pos, int k,
+                            int dst_rows, cudaStream_t st) {
+  QuantArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.rows = rows;
+  a.rows_pad = pos == nullptr ? (rows + 127) / 128 * 128 : rows;
+  a.K = K;
+  a.kb = scale_tiles(fmt, K);
+  a.c_pad = a.kb * (fmt == HQ_FP4_NV ? 4 : 8);
+  a.lanes_log = 3;  // whole scale words within a warp
+  while ((1 << a.lanes_log) < a.c_pad && a.lanes_log < 8) ++a.lanes_log;
+  a.ts = ts;
+  a.codes = codes;
+  a.scales = scales;
+  a.values = values;
+  a.pos = pos;
+  a.k = k;
+  a.dst_rows = dst_rows;
+  const int per = kThreads >> a.lanes_log;
+  const dim3 grid((a.rows_pad + per - 1) / per, (a.c_pad + (1 << a.lanes_log) - 1) >> a.lanes_log);
+  switch (xd) {
+    case HQ_F16: return quantize_launch<__half>(fmt, a, grid, st);
+    case HQ_BF16: return quantize_launch<__nv_bfloat16>(fmt, a, grid, st);
+    default: return quantize_launch<float>(fmt, a, grid, st);
+  }
+}
+
+hq_status check_rows(const void* x, hq_dtype xd, size_t ldx, int K) {
+  if (xd < HQ_F16 || xd > HQ_F32) return HQ_ERR_INVALID_ARG;
+  const size_t es = xd == HQ_F32 ? 4 : 2;
+  if (x == nullptr || (reinterpret_cast<uintptr_t>(x) & 15) != 0) return HQ_ERR_INVALID_ARG;
+  if (ldx < static_cast<size_t>(K) || (ldx * es) % 16 != 0 || ldx > (size_t{1} << 40)) return HQ_ERR_INVALID_ARG;
+  return HQ_OK;
+}
+
+hq_status check_shape(int fmt, long rows, int K) {
+  if (fmt != HQ_FP4_NV && fmt != HQ_FP4_MX) return HQ_ERR_INVALID_ARG;
+  if (rows < 0 || rows > (1 << 28) || K <= 0) return HQ_ERR_INVALID_ARG;
+  if (K % 32 != 0 || K > (1 << 17)) return HQ_ERR_UNSUPPORTED;
+  return HQ_OK;
+}
+
+hq_status check_matrix(const hq_fp4_matrix* m) {
+  if (m == nullptr) return HQ_ERR_INVALID_ARG;
+  const hq_status s = check_shape(m->format, m->rows, m->K);
+  if (s != HQ_OK) return s;
+  if (m->rows > 0 && (m->codes == nullptr || m->scales == nullptr)) return HQ_ERR_INVALID_ARG;
+  auto bad = [](const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; };
+  if (bad(m->codes, 16) || bad(m->scales, 16) || bad(m->tensor_scale, 4)) return HQ_ERR_INVALID_ARG;
+  if (m->tensor_scale != nullptr && (m->format != HQ_FP4_NV || m->n_tensor_scales < 1)) return HQ_ERR_INVALID_ARG;
+  return HQ_OK;
+}
+
+}  // namespace fp4
+}  // namespace hq
+
+using namespace hq;
+
+extern "C" {
+
+size_t hq_fp4_scale_bytes(int format, int rows, int K) {
+  if (fp4::check_shape(format, rows, K) != HQ_OK) return 0;
+  return fp4::scale_bytes(format, rows, K);
+}
+
+hq_status hq_fp4_quantize(const void* x, hq_dtype x_dtype, size_t ldx, const hq_fp4_matrix* q, void* values,
+                          hq_stream_t stream) {
+  const hq_status ok = fp4::check_matrix(q);
+  if (ok != HQ_OK) return ok;
+  if (q->tensor_scale != nullptr && q->n_tensor_scales != 1) return HQ_ERR_UNSUPPORTED;
+  if (q->rows == 0) return HQ_OK;
+  const hq_status rows_ok = fp4::check_rows(x, x_dtype, ldx, q->K);
+  if (rows_ok != HQ_OK) return rows_ok;
+  if (values != nullptr && (reinterpret_cast<uintptr_t>(values) & 15) != 0) return HQ_ERR_INVALID_ARG;
+  return from_cuda(fp4::launch_quantize(q->format, x_dtype, x, ldx, q->rows, q->K, q->tensor_scale, q->codes,
+                                        q->scales, values, nullptr, 1, q->rows,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+hq_status hq_fp4_tensor_scale(const void* x, hq_dtype x_dtype, size_t ldx, int rows, int K, float* scale,
+                              void* workspace, size_t ws_bytes, hq_stream_t stream) {
+  const hq_status ok = fp4::check_shape(HQ_FP4_NV, rows, K);
+  if (ok != HQ_OK) return ok;
+  if (rows == 0) return HQ_ERR_INVALID_ARG;
+  const hq_status rows_ok = fp4::check_rows(x, x_dtype, ldx, K);
+  if (rows_ok != HQ_OK) return rows_ok;
+  if (scale == nullptr || (reinterpret_cast<uintptr_t>(scale) & 3) != 0) return HQ_ERR_INVALID_ARG;
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || ws_bytes < 256) {
+    return HQ_ERR_WORKSPACE;
+  }
+  const int chunks = K / 16;
+  const size_t blocks = (static_cast<size_t>(rows) * chunks + fp4::kThreads - 1) / fp4::kThreads;
+  const int grid = static_cast<int>(std::min<size_t>(blocks, static_cast<size_t>(sm_count()) * 8));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t* ws = static_cast<uint32_t*>(workspace);
+  auto go = [&](auto* p) {
+    using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+    return launch_pdl(fp4::tensor_scale_kernel<T>, dim3(grid), dim3(fp4::kThreads), 0, st, true, p, ldx, rows,
+                      chunks, scale, ws);
+  };
+  switch (x_dtype) {
+    case HQ_F16: return from_cuda(go(static_cast<const __half*>(x)));
+    case HQ_BF16: return from_cuda(go(static_cast<const __nv_bfloat16*>(x)));
+    default: return from_cuda(go(static_cast<const float*>(x)));
+  }
+}
+
+}  // extern "C"

@@ -42,12 +42,6 @@ static_assert(kG32SyncWord >= kMaxTcGrid && (kG32SyncWord + 2) * 4 <= static_cas
               "gate words inside the counter region, past the tensor-core counters");
 constexpr int kMaxColBlock = 8;
 
-static hq_status from_cuda(cudaError_t e) {
-  if (e == cudaSuccess) return HQ_OK;
-  (void)cudaGetLastError();  // clear a non-sticky launch error
-  return HQ_ERR_CUDA;
-}
-
 static hq_status check_weight(const hq_weight* w) {
   if (w == nullptr) return HQ_ERR_INVALID_ARG;
   if (w->M <= 0 || w->K <= 0 || w->M > (1 << 28)) return HQ_ERR_INVALID_ARG;

@@ -18,6 +18,14 @@ enum : uint32_t {
   HQ_DEV_BAD_ZERO = 8u,
 };
 
+// The status of a launch or runtime call (a launch error that is not sticky is
+// cleared).
+inline hq_status from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return HQ_OK;
+  (void)cudaGetLastError();
+  return HQ_ERR_CUDA;
+}
+
 // Counts every kernel launch libhq enqueues (hq_launch_count).
 void note_launch();
 // True (and one fewer pending) if hq_set_test_fault asked for a withheld copy.

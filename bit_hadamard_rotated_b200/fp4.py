@@ -1,0 +1,216 @@
+"""Microscaled 4-bit floating-point matrices (include/hq.h, hq_fp4_*).
+
+As everywhere in this package: checks of devices, types and shapes, pointer
+marshalling and the tensors' own device's current stream.  Nothing is computed
+here.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._lib import HQ_FP4_MX, HQ_FP4_NV, HqFp4Matrix, check, lib
+from .hq import _DT, _need_cuda, _ptr, _raw_stream
+
+_FMT = {"nv": HQ_FP4_NV, "mx": HQ_FP4_MX}
+
+
+def _scale_shape(fmt: str, rows: int, K: int):
+    """Scale tiles [row tiles][K tiles][32][4][4] (include/hq.h)."""
+    return (rows + 127) // 128, -(-K // (64 if fmt == "nv" else 128)), 32, 4, 4
+
+
+def _need_scale(t, dev, n=1):
+    if t is not None and (t.dtype != torch.float32 or t.numel() not in (1, n) or not t.is_contiguous()
+                          or t.device != dev):
+        raise ValueError(f"a tensor scale must be fp32 with {'one value' if n == 1 else f'1 or {n} values'} on {dev}")
+
+
+class Fp4Matrix:
+    """A packed matrix: codes uint8 [rows][K/2], scales uint8 tiles [row
+    tiles][K tiles][32][4][4], fmt "nv" or "mx", tensor_scale fp32 (one value,
+    or one per expert) or None.  values: the rounded values, where
+    hq_fp4_quantize was asked for them."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: str = "nv",
+                 tensor_scale: torch.Tensor | None = None, values: torch.Tensor | None = None):
+        _need_cuda(codes, scales, tensor_scale)
+        if fmt not in _FMT:
+            raise ValueError('fmt must be "nv" or "mx"')
+        if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous():
+            raise ValueError("codes must be a contiguous uint8 [rows][K/2] tensor")
+        rows, K = codes.shape[0], codes.shape[1] * 2
+        if (scales.dtype != torch.uint8 or tuple(scales.shape) != _scale_shape(fmt, rows, K)
+                or not scales.is_contiguous() or scales.device != codes.device):
+            raise ValueError(f"scales must be contiguous uint8 tiles {_scale_shape(fmt, rows, K)} on {codes.device}")
+        if tensor_scale is not None and (fmt != "nv" or tensor_scale.dtype != torch.float32 or tensor_scale.numel() < 1
+                                         or not tensor_scale.is_contiguous() or tensor_scale.device != codes.device):
+            raise ValueError(f'tensor_scale must be contiguous fp32 on {codes.device}, and only for "nv"')
+        self._set(codes, scales, fmt, tensor_scale, values)
+
+    def _set(self, codes, scales, fmt, tensor_scale, values):
+        self.codes, self.scales, self.fmt, self.tensor_scale, self.values = codes, scales, fmt, tensor_scale, values
+        self.c = HqFp4Matrix(_FMT[fmt], codes.shape[0], codes.shape[1] * 2, codes.data_ptr(), scales.data_ptr(),
+                             None if tensor_scale is None else tensor_scale.data_ptr(),
+                             0 if tensor_scale is None else tensor_scale.numel())
+        self._ref = ctypes.byref(self.c)
+        return self
+
+    @property
+    def rows(self):
+        return self.c.rows
+
+    @property
+    def K(self):
+        return self.c.K
+
+
+def _rows_in(x, K=None):
+    """x as rows the kernels read: 2-D, fp16/bf16/fp32, unit stride along K and
+    rows on 16-byte boundaries (copied if they are not)."""
+    if x.dtype not in _DT or x.dim() != 2 or (K is not None and x.shape[1] != K):
+        raise ValueError(f"x must be fp16, bf16 or fp32 [rows][{'K' if K is None else K}]")
+    if x.is_contiguous():
+        return x if x.data_ptr() % 16 == 0 else x.clone()
+    if x.stride(1) == 1 and x.stride(0) >= x.shape[1] and x.stride(0) * x.element_size() % 16 == 0 and x.data_ptr() % 16 == 0:
+        return x
+    return x.contiguous()
+
+
+def hq_fp4_tensor_scale(x: torch.Tensor, stream=None) -> torch.Tensor:
+    """max |x| / 2688 as an fp32 scalar tensor: the tensor scale that puts x's
+    largest block at the end of the "nv" format's range (1 for zeros)."""
+    _need_cuda(x)
+    x = _rows_in(x)
+    with torch.cuda.device(x.device):
+        out = torch.empty((), dtype=torch.float32, device=x.device)
+        ws = torch.zeros(256, dtype=torch.uint8, device=x.device)
+        check(lib().hq_fp4_tensor_scale(_ptr(x), _DT[x.dtype], max(x.stride(0), x.shape[1]), x.shape[0], x.shape[1], _ptr(out),
+                                        _ptr(ws), 256, _raw_stream(stream, x.device.index)), "hq_fp4_tensor_scale")
+    return out
+
+
+def hq_fp4_quantize(x: torch.Tensor, fmt: str = "nv", tensor_scale: torch.Tensor | None = None, values=False,
+                    stream=None) -> Fp4Matrix:
+    """Pack rows x [rows][K] (fp16/bf16/fp32, K a multiple of 32).  values: True,
+    or a tensor like x to write into, for the rounded values in x's type too."""
+    _need_cuda(x, tensor_scale)
+    if fmt not in _FMT:
+        raise ValueError('fmt must be "nv" or "mx"')
+    x = _rows_in(x)
+    rows, K = x.shape
+    dev = x.device
+    if tensor_scale is not None:
+        if fmt != "nv":
+            raise ValueError('only "nv" takes a tensor scale')
+        _need_scale(tensor_scale, dev)
+    with torch.cuda.device(dev):
+        if values is True:
+            values = torch.empty((rows, K), dtype=x.dtype, device=dev)
+        elif values is False:
+            values = None
+        elif values is not None and (values.dtype != x.dtype or values.shape != x.shape or not values.is_contiguous()
+                                     or values.device != dev):
+            raise ValueError("values must be a contiguous tensor of x's type and shape")
+        q = Fp4Matrix.__new__(Fp4Matrix)._set(
+            torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
+            torch.empty(_scale_shape(fmt, rows, K), dtype=torch.uint8, device=dev), fmt, tensor_scale, values)
+        q.c.K = K  # as given: an odd K is refused below
+        check(lib().hq_fp4_quantize(_ptr(x), _DT[x.dtype], max(x.stride(0), K), q._ref, _ptr(values),
+                                    _raw_stream(stream, dev.index)), "hq_fp4_quantize")
+    return q
+
+
+def _out(out, rows, M, dtype, dev):
+    """The output and its row stride (rows may be strided, columns not)."""
+    if dtype not in _DT:
+        raise ValueError("the output must be fp16, bf16 or fp32")
+    if out is None:
+        return torch.empty((rows, M), dtype=dtype, device=dev), M
+    if out.dtype != dtype or tuple(out.shape) != (rows, M) or out.device != dev or (M > 1 and out.stride(1) != 1) \
+            or (rows > 1 and out.stride(0) < M):
+        raise ValueError(f"out must be {dtype} [{rows}][{M}] on {dev} with unit column stride")
+    return out, max(out.stride(0), M)
+
+
+def _workspace(ws, need, dev):
+    if ws is None:
+        ws = torch.empty(max(need, 2048), dtype=torch.uint8, device=dev)
+        ws[:2048].zero_()  # the status word and the counters: all that has to be zero
+        return ws
+    if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    return ws
+
+
+def hq_fp4_matmul(w: Fp4Matrix, a: Fp4Matrix, out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[n][m] = sum_k w[m][k] a[n][k] of two packed matrices, [a.rows][w.rows]."""
+    dev = w.codes.device
+    if a.codes.device != dev:
+        raise ValueError(f"a is on {a.codes.device}, the weights on {dev}")
+    with torch.cuda.device(dev):
+        out, ldy = _out(out, a.rows, w.rows, out_dtype if out is None else out.dtype, dev)
+        ws = _workspace(workspace, int(lib().hq_fp4_matmul_workspace_size(w._ref, a.rows)), dev)
+        check(lib().hq_fp4_matmul(w._ref, a._ref, _ptr(out), _DT[out.dtype], ldy, _ptr(ws), ws.numel(),
+                                  _raw_stream(stream, dev.index)), "hq_fp4_matmul")
+    return out
+
+
+def hq_fp4_linear(w: Fp4Matrix, x: torch.Tensor, x_scale: torch.Tensor | None = None,
+                  out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = W q(x): x [N][K] (fp16/bf16/fp32) quantised row by row in w's format
+    (x_scale: its tensor scale), times the packed weights; [N][w.rows] of x's
+    type unless out_dtype says otherwise."""
+    _need_cuda(x, x_scale)
+    dev = w.codes.device
+    x = _rows_in(x, w.K)
+    if x.device != dev:
+        raise ValueError(f"x is on {x.device}, the weights on {dev}")
+    _need_scale(x_scale, dev)
+    N = x.shape[0]
+    with torch.cuda.device(dev):
+        out, ldy = _out(out, N, w.rows, (x.dtype if out is None else out.dtype) if out_dtype is None else out_dtype, dev)
+        ws = _workspace(workspace, int(lib().hq_fp4_linear_workspace_size(w._ref, N)), dev)
+        check(lib().hq_fp4_linear(w._ref, _ptr(x), _DT[x.dtype], max(x.stride(0), w.K), N, _ptr(x_scale), _ptr(out),
+                                  _DT[out.dtype], ldy, _ptr(ws), ws.numel(), _raw_stream(stream, dev.index)),
+              "hq_fp4_linear")
+    return out
+
+
+class Fp4Linear:
+    """A packed linear layer with its workspace: y = W q(x) (hq_fp4_linear).
+    x_scale: the activations' tensor scale ("nv"), or None.  One layer serves
+    one stream at a time."""
+
+    def __init__(self, w: Fp4Matrix, x_scale: torch.Tensor | None = None, out_dtype: torch.dtype | None = None):
+        self.w, self.x_scale, self.out_dtype = w, x_scale, out_dtype
+        _need_scale(x_scale, w.codes.device)
+        self._ws, self._batch = None, 0
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        w = self.w
+        dev = w.codes.device
+        if not x.is_cuda or x.device != dev:
+            raise ValueError(f"x is on {x.device}, the weights on {dev}")
+        x = _rows_in(x, w.K)
+        N = x.shape[0]
+        with torch.cuda.device(dev):
+            if N > self._batch or self._ws is None:  # a workspace for N serves every smaller batch
+                self._ws, self._batch = _workspace(None, int(lib().hq_fp4_linear_workspace_size(w._ref, N)), dev), N
+            out, ldy = _out(out, N, w.rows, self.out_dtype or (x.dtype if out is None else out.dtype), dev)
+            st = lib().hq_fp4_linear(w._ref, x.data_ptr(), _DT[x.dtype], max(x.stride(0), w.K), N, _ptr(self.x_scale),
+                                     out.data_ptr(), _DT[out.dtype], ldy, self._ws.data_ptr(), self._ws.numel(),
+                                     _raw_stream(stream, dev.index))
+            if st:
+                check(st, "hq_fp4_linear")
+        return out
+
+    def check_status(self, stream=None):
+        if self._ws is not None:
+            check(lib().hq_check_status(_ptr(self._ws), _raw_stream(stream, self._ws.device.index)), "device status")
+
+
+__all__ = ["Fp4Matrix", "Fp4Linear", "hq_fp4_tensor_scale", "hq_fp4_quantize", "hq_fp4_matmul", "hq_fp4_linear"]

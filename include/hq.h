@@ -369,6 +369,136 @@ hq_status hq_kv_attend(const hq_kv_cache* cache, int n_tokens, const uint16_t* q
 hq_status hq_to_bitplanes(const uint32_t* packed, size_t n_codes, uint32_t* planes,
                           hq_stream_t stream);
 
+/*
+ * Microscaled 4-bit floating point.  A matrix of E2M1 values (0, .5, 1, 1.5,
+ * 2, 3, 4, 6 with a sign) with one scale per block of consecutive k, the
+ * operand format of the 5th-generation tensor cores, for weights and
+ * activations alike.  (The pages' formats are integers with 16-bit
+ * activations; this one is the library's own.  In the rotated basis that
+ * hq_rotate makes, outliers are spread, which is what lets 4-bit activations
+ * hold.)
+ *   HQ_FP4_NV  blocks of 16, E4M3 scales, times an optional fp32 tensor scale
+ *   HQ_FP4_MX  blocks of 32, power-of-two scales (E8M0: 2^(byte - 127))
+ * Values: code * scale (* tensor scale).  codes: [rows][K/2] bytes, k even in
+ * the low nibble; bit 3 of a code is the sign, bits 0-2 index the magnitudes.
+ * scales: tiles of 128 rows x 4 consecutive blocks, 512 bytes; with KB =
+ * ceil(K / 64) (NV) or ceil(K / 128) (MX) tiles along K, block j of row r is
+ * the byte at ((r / 128) * KB + j / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4
+ * + j % 4; hq_fp4_scale_bytes gives the size.  Bytes that pad a tile along K
+ * are zero, bytes of rows past the last are never used.
+ */
+typedef enum { HQ_FP4_NV = 0, HQ_FP4_MX = 1 } hq_fp4_format;
+
+typedef struct {
+  int format;                /* hq_fp4_format */
+  int rows;                  /* 0 <= rows <= 2^28 */
+  int K;                     /* a multiple of 32 (HQ_ERR_UNSUPPORTED otherwise), <= 2^17 */
+  uint8_t* codes;            /* 16-byte aligned */
+  uint8_t* scales;           /* 16-byte aligned */
+  const float* tensor_scale; /* device, NV only; NULL: 1 */
+  int n_tensor_scales;       /* how many tensor_scale holds: 1, or (hq_fp4_experts) one per expert */
+} hq_fp4_matrix;
+
+/* Bytes of `scales` for a matrix of these sizes (0 on a bad argument). */
+size_t hq_fp4_scale_bytes(int format, int rows, int K);
+
+/*
+ * hq_fp4_quantize -- rows of real values to codes and scales, written into the
+ * caller's q->codes and q->scales.  Per block, in IEEE single precision, with
+ * t = *q->tensor_scale (1 if NULL):
+ *   NV:  scale = E4M3(amax / (6 t)), at most 448;  e = scale * t
+ *   MX:  scale = 2^max(floor(log2 amax) - 2, -127);  e = scale
+ *   code = E2M1(x / e), at most 6 in magnitude, the sign of x (0 where e = 0)
+ * every rounding to nearest, ties to even.  A block that holds an infinity or
+ * a NaN gets the format's NaN as its scale (0x7F, 0xFF) and zero codes, so
+ * that it makes every product it enters NaN.
+ * x: [rows][K] of x_dtype, row stride ldx elements (>= K; rows start on
+ * 16-byte boundaries).  values: NULL, or [rows][K] of x_dtype, 16-byte
+ * aligned: the values that codes and scales stand for, rounded to x_dtype
+ * (what a quantised matrix is evaluated or trained against).
+ */
+hq_status hq_fp4_quantize(const void* x, hq_dtype x_dtype, size_t ldx, const hq_fp4_matrix* q, void* values,
+                          hq_stream_t stream);
+
+/* hq_fp4_tensor_scale -- *scale = max |x| / 2688 (6 * 448: the largest block
+ * scale then meets the largest value), 1 where that is 0.  x as in
+ * hq_fp4_quantize, rows >= 1.  workspace: 256 bytes, zero-filled before its
+ * first use; calls leave it zero. */
+hq_status hq_fp4_tensor_scale(const void* x, hq_dtype x_dtype, size_t ldx, int rows, int K, float* scale,
+                              void* workspace, size_t ws_bytes, hq_stream_t stream);
+
+/* Bytes of workspace hq_fp4_matmul needs for n_rows rows of a (0 on a bad
+ * argument); enough for fewer rows too.  Of a workspace of the hq_fp4 products
+ * only the first 2048 bytes have to be zero before its first use. */
+size_t hq_fp4_matmul_workspace_size(const hq_fp4_matrix* w, int n_rows);
+
+/*
+ * hq_fp4_matmul -- y[n][m] = sum_k w[m][k] a[n][k] of two packed matrices of
+ * one format and K, summed in fp32 by the tensor cores and rounded once to
+ * y_dtype.  y: [a->rows][w->rows], row stride ldy elements (>= w->rows),
+ * element-aligned.  a->rows = 0 launches nothing.
+ */
+hq_status hq_fp4_matmul(const hq_fp4_matrix* w, const hq_fp4_matrix* a, void* y, hq_dtype y_dtype, size_t ldy,
+                        void* workspace, size_t ws_bytes, hq_stream_t stream);
+
+/* Bytes of workspace hq_fp4_linear needs (0 on a bad argument). */
+size_t hq_fp4_linear_workspace_size(const hq_fp4_matrix* w, int batch);
+
+/*
+ * hq_fp4_linear -- y = W q(x): the activations are quantised as
+ * hq_fp4_quantize does it (with *x_scale as their tensor scale; NULL: 1), then
+ * multiplied as in hq_fp4_matmul.  x: [batch][K], row stride ldx, as in
+ * hq_fp4_quantize.
+ */
+hq_status hq_fp4_linear(const hq_fp4_matrix* w, const void* x, hq_dtype x_dtype, size_t ldx, int batch,
+                        const float* x_scale, void* y, hq_dtype y_dtype, size_t ldy, void* workspace,
+                        size_t ws_bytes, hq_stream_t stream);
+
+/* Kernels one hq_fp4_linear call enqueues. */
+int hq_fp4_linear_launches(void);
+
+/*
+ * Tokens sorted by expert and back: the steps that hq_moe_experts takes
+ * inside, for callers that run their own products between them.
+ *
+ * hq_moe_sort -- a row for every (token, slot) pair: the pairs of expert e, in
+ * the order of their index t*k + j, take rows offsets[e], offsets[e] + 1, ...;
+ * segments follow one another in the order of the experts, each start a
+ * multiple of `align`.  An id outside [0, n_experts) gets no row (pos = -1:
+ * a masked token, or an expert that lives elsewhere).
+ * topk_ids: int32 [T][k].  pos: int32 [T][k].  offsets: int32 [n_experts + 1],
+ * the last one the end of the last segment, rounded up like every start.
+ * counts: int32 [n_experts].  Rows used are below T*k + min(n_experts, T*k) *
+ * (align - 1) + 1.  1 <= k <= 32, n_experts <= 16384, align <= 4096, T*k <=
+ * 2^23 (HQ_ERR_UNSUPPORTED above).  workspace: >= hq_moe_sort_workspace_size.
+ */
+size_t hq_moe_sort_workspace_size(int T, int k, int n_experts);
+hq_status hq_moe_sort(const int32_t* topk_ids, int T, int k, int n_experts, int align, int32_t* pos,
+                      int32_t* offsets, int32_t* counts, void* workspace, size_t ws_bytes, hq_stream_t stream);
+
+/* hq_moe_gather -- rows[pos[t][j]] = x[t].  x [T][H], rows [n_rows][H], both
+ * of `dtype`; positions outside [0, n_rows) are skipped and rows without a
+ * pair are left as they were.  Its gradient is hq_moe_combine with topk_w =
+ * NULL. */
+hq_status hq_moe_gather(const void* x, hq_dtype dtype, const int32_t* pos, int T, int k, int H, void* rows,
+                        int n_rows, hq_stream_t stream);
+
+/* hq_moe_combine -- y[t] = sum_j topk_w[t][j] rows[pos[t][j]], slots in
+ * ascending order in fp32, rounded once; topk_w NULL: plain sums.  Slots whose
+ * position is outside [0, n_rows) add nothing.  y_dtype: `dtype`, or one of the
+ * two HQ_F32 (HQ_ERR_UNSUPPORTED otherwise). */
+hq_status hq_moe_combine(const void* rows, hq_dtype dtype, int n_rows, const int32_t* pos, const float* topk_w,
+                         int T, int k, int H, void* y, hq_dtype y_dtype, hq_stream_t stream);
+
+/* hq_moe_combine_grad -- the gradients of hq_moe_combine for dy [T][H]:
+ *   drows[pos[t][j]] = topk_w[t][j] dy[t],  dw[t][j] = sum_h dy[t][h]
+ *   rows[pos[t][j]][h]   (fp32; 0 for slots without a row)
+ * dy, rows and drows of `dtype`; rows of drows without a pair are left as they
+ * were.  Positions must not repeat (hq_moe_sort's do not). */
+hq_status hq_moe_combine_grad(const void* dy, hq_dtype dtype, const void* rows, int n_rows, const int32_t* pos,
+                              const float* topk_w, int T, int k, int H, void* drows, float* dw,
+                              hq_stream_t stream);
+
 /* Intermediates an hq_moe_experts call leaves in its workspace, for checking
  * the layer stage by stage:
  *   HQ_MOE_POS  int32 [T*k]: row of pair (t, j) (index t*k + j) in the two

@@ -1,0 +1,312 @@
+"""GPU parity of the microscaled 4-bit matrices (hq_fp4_*) against the 64-bit
+oracle.
+
+Codes and scales are decided in IEEE single precision on both sides and must
+match bit for bit.  A product's operands are exact (codes times scales have at
+most 6 significant bits, so every product of two is exact in fp32), which
+leaves the sums: K terms in fp32, each addition off by at most an ulp of the
+partial sum (the tensor cores may truncate, 2^-23), the two tensor scales
+(3 roundings of 2^-24) and one rounding of the result to y's type:
+  tol = ((K + 64) 2^-23 + 3 2^-24) sum_k |w_k a_k| + eps(y) / 2 (|y| + that) + tiny(y)
+with tiny half a step of y's smallest numbers (2^-25 in fp16).
+"""
+import numpy as np
+import pytest
+import torch
+
+from bit_hadamard_rotated_b200 import (Fp4Linear, Fp4Matrix, HqError, hq_fp4_linear, hq_fp4_matmul, hq_fp4_quantize,
+                                       hq_fp4_tensor_scale, hq_launch_count, hq_rotate)
+from oracle import fp4
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_hadamard_rotated_b200 import build
+    build.build()
+
+
+def rows(R, K, dtype, seed, scale=1.0):
+    """N(0, 1) rows, 1 % of the channels x 20, a zero row, a zero block, exact
+    multiples of small steps (ties between codes and between scales)."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((R, K)) * scale
+    x[:, rng.choice(K, max(1, K // 100), replace=False)] *= 20
+    if R > 2:
+        x[1] = 0
+        x[2] = rng.integers(-24, 25, K) / 4 * scale
+    x[0, :32] = 0
+    return torch.from_numpy(x).to(dtype)
+
+
+def bits(t):
+    return t.cpu().numpy()
+
+
+def check_quantised(q, x, fmt, ts=None):
+    R, K = x.shape
+    c, s, v = fp4.quantize(x.double().numpy(), fmt, ts)
+    assert np.array_equal(bits(q.codes), fp4.pack(c))
+    assert np.array_equal(bits(q.scales), fp4.tile(s))
+    if q.values is not None:
+        want = torch.from_numpy(v)
+        got = q.values.cpu().double()
+        # one rounding to x's type, after the fp32 product code * e (2^-24)
+        tol = (torch.finfo(x.dtype).eps / 2 + 2.0**-24) * want.abs() * (1 + 2.0**-10) + 2.0**-149
+        if x.dtype == torch.float16:
+            tol = tol + 2.0**-25
+        ok = ((got - want).abs() <= tol) | (torch.isnan(got) & torch.isnan(want))
+        assert bool(ok.all())
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("R,K", [(1, 32), (1, 8192), (3, 96), (33, 4128), (130, 160), (257, 1024), (5, 16384)])
+def test_quantize_bit_exact(fmt, dtype, R, K):
+    x = rows(R, K, dtype, R + K)
+    check_quantised(hq_fp4_quantize(x.cuda(), fmt, values=True), x, fmt)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("ts", [1.0, 0.0073, 3.1e-5, 2.0**-40, 2.0**90])
+def test_quantize_tensor_scale_bit_exact(dtype, ts):
+    x = rows(40, 512, dtype, 7, scale=min(ts * 50, 1000.0))
+    t = torch.tensor(ts, dtype=torch.float32, device="cuda")
+    q = hq_fp4_quantize(x.cuda(), "nv", tensor_scale=t, values=dtype == torch.float32)
+    check_quantised(q, x, "nv", ts)
+
+
+def test_quantize_every_tie_and_neighbour():
+    """fp32 values on and one ulp beside every border between codes, for every
+    E4M3 block scale: the quotient's last bit decides."""
+    mids = (fp4.GRID[1:] + fp4.GRID[:-1]) / 2
+    x = np.zeros((126, 32), dtype=np.float32)
+    for r, s in enumerate(fp4._E4M3[1:]):
+        m = (mids * s).astype(np.float32)
+        x[r, 0] = x[r, 16] = 6 * s
+        x[r, 1:8], x[r, 8:15] = m, np.nextafter(m, np.float32(np.inf))
+        x[r, 17:24], x[r, 24:31] = -m, -np.nextafter(m, np.float32(0))
+    t = torch.from_numpy(x)
+    check_quantised(hq_fp4_quantize(t.cuda(), "nv"), t, "nv")
+    u = t * 1.37e-3
+    ts = 1.37e-3
+    check_quantised(hq_fp4_quantize(u.cuda(), "nv", tensor_scale=torch.tensor(ts, device="cuda")), u, "nv", ts)
+
+
+def test_quantize_extremes():
+    """Subnormals, the largest values, infinities, NaN, negative zeros."""
+    x = np.zeros((8, 64), dtype=np.float32)
+    x[0, :16] = 2.0**-149
+    x[1] = np.linspace(-3.4e38, 3.4e38, 64)
+    x[2, 5], x[3, 40], x[4, 63] = np.inf, -np.inf, np.nan
+    x[2, 20:], x[5] = 1.0, -0.0
+    x[6, :32], x[6, 32:] = 2.0**-126, 1e-30
+    x[7] = np.linspace(-1e-3, 1e-3, 64)
+    t = torch.from_numpy(x)
+    for fmt in ("nv", "mx"):
+        check_quantised(hq_fp4_quantize(t.cuda(), fmt, values=True), t, fmt)
+
+
+def test_quantize_strided_rows_and_refusals():
+    big = rows(20, 512, torch.bfloat16, 3).cuda()
+    part = big[:, 128:416]
+    a, b = hq_fp4_quantize(part, "mx"), hq_fp4_quantize(part.contiguous(), "mx")
+    assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+    odd = big[:, 1:129]  # rows off 16-byte boundaries: copied by the binding
+    assert torch.equal(hq_fp4_quantize(odd).codes, hq_fp4_quantize(odd.contiguous()).codes)
+    with pytest.raises(HqError):
+        hq_fp4_quantize(big[:, :48].contiguous())
+    with pytest.raises(ValueError):
+        hq_fp4_quantize(big, "mx", tensor_scale=torch.ones((), device="cuda"))
+    with pytest.raises(ValueError):
+        hq_fp4_quantize(big.double())
+    n0 = hq_launch_count()
+    q = hq_fp4_quantize(big[:0])
+    assert q.codes.shape == (0, 256) and q.scales.shape[0] == 0 and hq_launch_count() == n0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("R,K", [(1, 32), (77, 4128), (3000, 2048)])
+def test_tensor_scale(dtype, R, K):
+    x = rows(R, K, dtype, R, 0.02).cuda()
+    want = np.float32(x.double().abs().max().item() / 2688.0 or 1)
+    assert hq_fp4_tensor_scale(x).item() == want
+    assert hq_fp4_tensor_scale(torch.zeros_like(x)).item() == 1.0
+    assert hq_fp4_tensor_scale(x[:, :32]).item() == np.float32(x[:, :32].double().abs().max().item() / 2688.0 or 1)
+
+
+# ------------------------------------------------------------------ products
+
+
+def weight(M, K, fmt, seed, scaled):
+    w = rows(M, K, torch.float32, seed, K**-0.5).cuda()
+    ts = hq_fp4_tensor_scale(w) if scaled else None
+    return hq_fp4_quantize(w, fmt, tensor_scale=ts)
+
+
+def dense(q):
+    ts = None if q.tensor_scale is None else q.tensor_scale.cpu().numpy()
+    return fp4.values(bits(q.codes), bits(q.scales), q.fmt, ts)
+
+
+def check_product(y, W, A, K):
+    want, base = A @ W.T, np.abs(A) @ np.abs(W).T
+    eps = torch.finfo(y.dtype).eps
+    sums = ((K + 64) * 2.0**-23 + 3 * 2.0**-24) * base
+    tol = sums + eps / 2 * (np.abs(want) + sums) + (2.0**-25 if y.dtype == torch.float16 else 2.0**-149)
+    got = y.double().cpu().numpy()
+    assert np.all(np.isfinite(got))
+    err = np.abs(got - want)
+    assert np.all(err <= tol), f"worst err/tol {np.max(err / tol):.3g} at {np.unravel_index(np.argmax(err / tol), err.shape)}"
+    return np.linalg.norm(err) / np.linalg.norm(want)
+
+
+SHAPES = [  # M, K, N
+    (128, 256, 16), (128, 256, 1), (1, 32, 1), (128, 64, 32), (128, 32, 8), (300, 96, 5), (128, 1024, 64), (384, 512, 33),
+    (4100, 4128, 2), (640, 8192, 1), (128, 2048, 128), (257, 1056, 129), (512, 512, 256), (1000, 736, 333), (2304, 4096, 70),
+    (129, 16384, 3), (256, 288, 1025), (20000, 256, 7),
+]
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_matmul_parity(fmt, M, K, N):
+    w = weight(M, K, fmt, M + K, fmt == "nv")
+    x = rows(N, K, torch.bfloat16, N).cuda()
+    a = hq_fp4_quantize(x, fmt)
+    y = hq_fp4_matmul(w, a)
+    torch.cuda.synchronize()
+    check_product(y, dense(w), dense(a), K)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("out", DTYPES)
+def test_linear_types(fmt, dtype, out):
+    M, K, N = 520, 1312, 37
+    w = weight(M, K, fmt, 5, fmt == "nv")
+    x = rows(N, K, dtype, 6)
+    xs = 0.031 if fmt == "nv" else None
+    t = None if xs is None else torch.tensor(xs, device="cuda")
+    y = hq_fp4_linear(w, x.cuda(), x_scale=t, out_dtype=out)
+    assert y.dtype == out
+    check_product(y, dense(w), fp4.quantize(x.double().numpy(), fmt, xs)[2], K)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_linear_equals_quantise_then_matmul(fmt, M, K, N):
+    """The layer's early weight reads change nothing; one layer and workspace for falling and rising batches."""
+    w = weight(M, K, fmt, M + K + 1, False)
+    layer = Fp4Linear(w, out_dtype=torch.float32)
+    x = rows(max(N, 3), K, torch.float16, N).cuda()
+    for n in (N, 1, N, min(N, 3)):
+        got = layer(x[:n])
+        assert torch.equal(got, hq_fp4_matmul(w, hq_fp4_quantize(x[:n], fmt)))
+    layer.check_status()
+
+
+def test_weights_packed_just_before_the_call():
+    """Packing and multiplying back to back, over and over on one stream, with the weights' buffers reused."""
+    ws = [rows(512, 2048, torch.float32, s, 0.03).cuda() for s in range(6)]
+    x = rows(4, 2048, torch.float32, 9).cuda()
+    want = [hq_fp4_matmul(hq_fp4_quantize(w), hq_fp4_quantize(x)).clone() for w in ws]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for w, y in zip(ws, want):
+            assert torch.equal(hq_fp4_linear(hq_fp4_quantize(w), x), y)
+
+
+def test_nan_and_infinity_reach_their_rows_only():
+    w = weight(200, 512, "nv", 1, False)
+    x = rows(40, 512, torch.float32, 2)
+    x[7, 100], x[9, 3], x[20, 511] = float("nan"), float("inf"), -float("inf")
+    y = hq_fp4_linear(w, x.cuda()).cpu()
+    bad = torch.isnan(y).all(1)
+    assert bad.nonzero().flatten().tolist() == [7, 9, 20]
+    assert bool(torch.isfinite(y[~bad]).all())
+
+
+def test_strided_output_and_rows():
+    w = weight(300, 512, "mx", 3, False)
+    big = rows(50, 1024, torch.bfloat16, 4).cuda()
+    out = torch.full((50, 400), 7.0, device="cuda")
+    y = hq_fp4_linear(w, big[:, 256:768], out=out[:, 50:350])
+    assert torch.equal(y, hq_fp4_linear(w, big[:, 256:768].contiguous(), out_dtype=torch.float32))
+    assert bool((out[:, :50] == 7).all()) and bool((out[:, 350:] == 7).all())
+
+
+def test_repeats_are_equal_and_streams_are_kept():
+    w = weight(2048, 4096, "nv", 8, True)
+    x = rows(5, 4096, torch.bfloat16, 9).cuda()
+    want = hq_fp4_linear(w, x)
+    layers = [Fp4Linear(w), Fp4Linear(w)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for lay, st in zip(layers, streams):
+            with torch.cuda.stream(st):
+                got.append(lay(x))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+
+
+def test_captured_and_replayed():
+    w = weight(1024, 2048, "nv", 10, True)
+    layer = Fp4Linear(w)
+    x = rows(3, 2048, torch.bfloat16, 11).cuda()
+    y = torch.empty(3, 1024, dtype=torch.bfloat16, device="cuda")
+    layer(x, out=y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer(x, out=y)
+    for s in range(4):
+        x.copy_(rows(3, 2048, torch.bfloat16, 20 + s))
+        g.replay()
+        assert torch.equal(y, hq_fp4_linear(w, x))
+
+
+def test_rotated_basis():
+    """Rotate, pack and multiply: (H W)(H x) = W x, so the packed product in the rotated basis is near W x."""
+    M, K, N = 256, 2048, 4
+    rng = np.random.default_rng(0)
+    s = torch.from_numpy((rng.integers(0, 2, K) * 2 - 1).astype(np.int8)).cuda()
+    W, x = rows(M, K, torch.float32, 1, K**-0.5).cuda(), rows(N, K, torch.float32, 2).cuda()
+    wr, xr = hq_rotate(W, s), hq_rotate(x, s)
+    w = hq_fp4_quantize(wr, "nv", tensor_scale=hq_fp4_tensor_scale(wr))
+    a = hq_fp4_quantize(xr)
+    y = hq_fp4_matmul(w, a)
+    check_product(y, dense(w), dense(a), K)
+    # each factor is off by at most half a step: 1/4 of its block's effective scale below 2, 1/2 below 4, 1 below 6,
+    # so by at most 1/6 of the block's largest magnitude and the scale's own rounding (2^-4) on saturated values
+    want = (x.double() @ W.double().T).cpu().numpy()
+    Wd, Ad = dense(w), dense(a)
+    dW, dA = np.abs(Wd - wr.double().cpu().numpy()), np.abs(Ad - xr.double().cpu().numpy())
+    bound = dA @ np.abs(Wd).T + np.abs(xr.double().cpu().numpy()) @ dW.T
+    rot = (14 * 2.0**-24) * (np.abs(x.double().cpu().numpy()).sum(1)[:, None] * np.abs(W.double().cpu().numpy()).sum(1)[None])
+    assert np.all(np.abs(y.double().cpu().numpy() - want) <= bound * (1 + 1e-6) + rot + 1e-4)
+
+
+def test_matmul_refusals():
+    w = weight(128, 256, "nv", 1, False)
+    a = hq_fp4_quantize(rows(4, 256, torch.float32, 2).cuda())
+    with pytest.raises(HqError):
+        hq_fp4_matmul(w, hq_fp4_quantize(rows(4, 256, torch.float32, 2).cuda(), "mx"))
+    with pytest.raises(HqError):
+        hq_fp4_matmul(w, hq_fp4_quantize(rows(4, 512, torch.float32, 2).cuda()))
+    with pytest.raises(HqError):
+        hq_fp4_matmul(w, a, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        hq_fp4_matmul(w, a, out=torch.empty(4, 100, device="cuda"))
+    with pytest.raises(ValueError):
+        hq_fp4_linear(w, torch.zeros(4, 128, device="cuda"))
+    with pytest.raises(ValueError):
+        Fp4Matrix(w.codes, w.scales[:, :1].contiguous())
+    n0 = hq_launch_count()
+    assert hq_fp4_linear(w, torch.zeros(0, 256, device="cuda")).shape == (0, 128) and hq_launch_count() == n0

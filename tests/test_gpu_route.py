@@ -1,0 +1,173 @@
+"""GPU parity of the routing steps (hq_moe_sort and the row movers) against the
+64-bit oracle.  Positions are integers and must be equal; gathered rows are
+copies; sums run over at most k = 32 terms in fp32 (each addition and product
+half an ulp: (2 k + 1) 2^-24 of the sum of magnitudes) and are rounded once;
+dw sums H products (in lanes and a tree: at most H + 5 roundings).
+"""
+import numpy as np
+import pytest
+import torch
+
+from bit_hadamard_rotated_b200 import (HqError, hq_moe_combine, hq_moe_combine_grad, hq_moe_gather,
+                                       hq_moe_gather_grad, hq_moe_sort)
+from oracle import fp4
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_hadamard_rotated_b200 import build
+    build.build()
+
+
+def routing(T, k, E, seed, masked=0.0, skew=False):
+    rng = np.random.default_rng(seed)
+    ids = np.stack([rng.permutation(max(E, k))[:k] % E for _ in range(T)]) if T else np.zeros((0, k), dtype=np.int64)
+    if skew and T:
+        ids[:, 0] = 0
+    if masked and T:
+        ids[rng.random(T) < masked] = -1
+        ids.reshape(-1)[rng.integers(0, T * k, max(1, T * k // 50))] = E + 3
+    return ids.astype(np.int32)
+
+
+CASES = [  # T, k, E, align, masked
+    (1, 1, 1, 1, 0), (1, 8, 256, 1, 0), (32, 8, 256, 1, 0), (32, 8, 256, 128, 0.3), (1000, 4, 60, 16, 0.2), (1024, 8, 8, 1, 0),
+    (1025, 8, 7, 3, 0), (5003, 8, 256, 128, 0.125), (40000, 8, 300, 1, 0.5), (3000, 2, 16384, 1, 0), (9000, 1, 1025, 64, 0),
+    (5, 32, 40, 1, 0), (0, 4, 9, 8, 0), (700, 3, 5, 1, 1.0), (70000, 1, 2, 1, 0),
+]
+
+
+@pytest.mark.parametrize("T,k,E,align,masked", CASES)
+def test_sort(T, k, E, align, masked):
+    ids = routing(T, k, E, T + k + E, masked, skew=T == 1000)
+    plan = hq_moe_sort(torch.from_numpy(ids).cuda(), E, align=align)
+    pos, off, cnt = fp4.sort(ids, E, align)
+    assert np.array_equal(plan.pos.cpu().numpy(), pos)
+    assert np.array_equal(plan.offsets.cpu().numpy(), off)
+    assert np.array_equal(plan.counts.cpu().numpy(), cnt)
+    assert off[-1] <= plan.n_rows or off[-1] - plan.n_rows < align
+    assert pos.max(initial=-1) < max(plan.n_rows, 1)
+
+
+def test_sort_same_expert_twice_in_a_token():
+    ids = np.array([[3, 3, 1], [1, 3, 1]], dtype=np.int32)
+    plan = hq_moe_sort(torch.from_numpy(ids).cuda(), 4)
+    assert plan.pos.cpu().tolist() == [[3, 4, 0], [1, 5, 2]]
+
+
+def rnd(shape, dtype, seed):
+    return torch.from_numpy(np.random.default_rng(seed).standard_normal(shape)).to(dtype)
+
+
+def near(got, want, sums, dtype, terms):
+    """|got - want| within `terms` roundings of the sum of magnitudes and one of the result."""
+    s = terms * 2.0**-24 * sums
+    tol = s + torch.finfo(dtype).eps / 2 * (np.abs(want) + s) + (2.0**-25 if dtype == torch.float16 else 2.0**-149)
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert np.all(err <= tol), float(np.max(err / tol))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,H,align,masked", [
+    (1, 1, 3, 8, 1, 0), (1, 8, 16, 2048, 1, 0), (32, 8, 256, 2048, 128, 0.3), (61, 5, 9, 999, 1, 0.2), (7, 32, 40, 33, 4, 0.5),
+    (300, 4, 60, 4096, 1, 0), (40, 2, 4, 1, 1, 0), (20, 3, 6, 9000, 1, 0.2), (12, 3, 6, 64, 1, 1.0),
+])
+def test_rows_there_and_back(dtype, T, k, E, H, align, masked):
+    ids = routing(T, k, E, T + H, masked)
+    plan = hq_moe_sort(torch.from_numpy(ids).cuda(), E, align=align)
+    pos, _, _ = fp4.sort(ids, E, align)
+    has, n = pos >= 0, plan.n_rows
+    x, dy, z, dxs = (rnd((r, H), dtype, i) for i, r in enumerate((T, T, n, n)))
+    w = rnd((T, k), torch.float32, 9)
+    z[np.setdiff1d(np.arange(n), pos[has])] = float("nan")  # rows without a pair are never read
+    dxs[np.setdiff1d(np.arange(n), pos[has])] = float("nan")
+    out = torch.full((n, H), 5.0, dtype=dtype, device="cuda")
+    xs = hq_moe_gather(x.cuda(), plan, out=out).cpu()
+    want = torch.full((n, H), 5.0, dtype=dtype)
+    t_of, j_of = np.nonzero(has)
+    want[pos[has]] = x[t_of]
+    assert torch.equal(xs, want)
+    xd, dyd, wd = x.double().numpy(), dy.double().numpy(), w.double().numpy()
+    zd = np.where(has[..., None], z.double().numpy()[pos], 0)
+    y = hq_moe_combine(z.cuda(), plan, w.cuda())
+    near(y, (wd[..., None] * zd).sum(1), np.abs(wd[..., None] * zd).sum(1), dtype, 2 * k + 1)
+    y32 = hq_moe_combine(z.cuda(), plan, w.cuda(), out_dtype=torch.float32)
+    near(y32, (wd[..., None] * zd).sum(1), np.abs(wd[..., None] * zd).sum(1), torch.float32, 2 * k + 1)
+    gd = np.where(has[..., None], dxs.double().numpy()[pos], 0)
+    near(hq_moe_gather_grad(dxs.cuda(), plan), gd.sum(1), np.abs(gd).sum(1), dtype, k)
+    out = torch.full((n, H), 5.0, dtype=dtype, device="cuda")
+    dz, dw = hq_moe_combine_grad(dy.cuda(), z.cuda(), plan, w.cuda(), out=out)
+    wdz = np.full((n, H), 5.0)
+    wdz[pos[has]] = wd[has][:, None] * dyd[t_of]
+    near(dz, wdz, np.abs(wdz), dtype, 1)
+    near(dw, (dyd[:, None] * zd).sum(2), np.abs(dyd[:, None] * zd).sum(2), torch.float32, H + 5)
+
+
+def test_gradients_against_differences():
+    """hq_moe_gather_grad and hq_moe_combine_grad are the gradients of gather
+    and combine: both are linear (or bilinear), so a difference over any step
+    is exact up to roundings."""
+    T, k, E, H = 6, 3, 5, 16
+    ids = routing(T, k, E, 1, 0.2)
+    plan = hq_moe_sort(torch.from_numpy(ids).cuda(), E)
+    n = plan.n_rows
+    x, z, w, dy, g = (rnd(s, torch.float32, i).cuda() for i, s in enumerate([(T, H), (n, H), (T, k), (T, H), (n, H)]))
+
+    def f_gather(v):
+        return (hq_moe_gather(v, plan, out=torch.zeros(n, H, device="cuda")).double() * g.double()).sum().item()
+
+    def f_combine(rows, weights):
+        return (hq_moe_combine(rows, plan, weights).double() * dy.double()).sum().item()
+
+    g0 = g.clone()
+    dx = hq_moe_gather_grad(g0, plan)
+    dz, dw = hq_moe_combine_grad(dy, z, plan, w, out=torch.zeros(n, H, device="cuda"))
+    for d, f, at in ((dx, f_gather, x), (dz, lambda v: f_combine(v, w), z), (dw, lambda v: f_combine(z, v), w)):
+        for i in np.random.default_rng(3).integers(0, at.numel(), 12):
+            e = torch.zeros_like(at).view(-1)
+            e[i] = 1.0
+            e = e.view_as(at)
+            diff = (f(at + e) - f(at - e)) / 2
+            # values of at + e are rounded to fp32 and summed over at most T k H terms of magnitude about 1
+            assert abs(diff - d.view(-1)[i].item()) <= 1e-4
+
+
+def test_refusals():
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    plan = hq_moe_sort(ids, 3)
+    x = torch.zeros((4, 8), device="cuda")
+    with pytest.raises(ValueError):
+        hq_moe_sort(ids.long(), 3)
+    with pytest.raises(HqError):
+        hq_moe_sort(ids, 0)
+    with pytest.raises(HqError):
+        hq_moe_sort(ids, 3, align=0)
+    with pytest.raises(HqError):
+        hq_moe_sort(torch.zeros((4, 33), dtype=torch.int32, device="cuda"), 3)
+    with pytest.raises(ValueError):
+        hq_moe_gather(x[:3], plan)
+    with pytest.raises(ValueError):
+        hq_moe_gather(x.double(), plan)
+    with pytest.raises(ValueError):
+        hq_moe_combine(x, plan, torch.zeros((4, 3), device="cuda"))
+    with pytest.raises(HqError):
+        hq_moe_combine(x.half(), plan, torch.zeros((4, 2), device="cuda"), out_dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        hq_moe_combine_grad(x, x.half(), plan, torch.zeros((4, 2), device="cuda"))
+
+
+def test_rows_outside_the_buffer_are_skipped():
+    """A buffer smaller than the plan's rows: what does not fit is neither written nor read."""
+    ids = routing(20, 4, 6, 3)
+    plan = hq_moe_sort(torch.from_numpy(ids).cuda(), 6)
+    x = rnd((20, 24), torch.float32, 1).cuda()
+    guard = torch.full((60, 24), 3.0, device="cuda")
+    out = hq_moe_gather(x, plan, out=guard[:40])
+    assert bool((guard[40:] == 3).all())
+    full = hq_moe_gather(x, plan)
+    assert torch.equal(out, full[:40])
