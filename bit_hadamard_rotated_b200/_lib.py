@@ -143,6 +143,12 @@ def lib() -> ctypes.CDLL:
         L.hq_fp4_linear.restype = _i
         L.hq_fp4_linear_launches.argtypes = []
         L.hq_fp4_linear_launches.restype = _i
+        L.hq_fp4_experts_workspace_size.argtypes = [pm, pm, pm, _i, _i, _i, _i]
+        L.hq_fp4_experts_workspace_size.restype = _sz
+        L.hq_fp4_experts.argtypes = [pm, pm, pm, _i, _vp, _i, _sz, _i, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _sz, _vp]
+        L.hq_fp4_experts.restype = _i
+        L.hq_fp4_experts_launches.argtypes = [_i, _i]
+        L.hq_fp4_experts_launches.restype = _i
         L.hq_moe_sort_workspace_size.argtypes = [_i, _i, _i]
         L.hq_moe_sort_workspace_size.restype = _sz
         L.hq_moe_sort.argtypes = [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]

@@ -31,6 +31,7 @@
 #include <algorithm>
 
 #include "fp4.cuh"
+#include "fp4_quant.cuh"
 #include "hq_common.cuh"
 #include "hq_internal.h"
 #include "hq_io.cuh"
@@ -45,6 +46,8 @@ namespace {
 constexpr int kM = 128;      // weight rows per tile
 constexpr int kChunk = 256;  // values of K per ring slot (128 bytes a row)
 constexpr int kWBytes = kM * kChunk / 2;
+constexpr int kTurnRow = 36;  // floats per token of an epilogue transpose (32 and padding)
+constexpr int kMaxGroups = 1024;
 
 // ------------------------------------------------------------------ PTX
 
@@ -93,23 +96,29 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
 
 // ------------------------------------------------------------------ plan
 
-template <int FMT, int NT>
+// What a launch computes: y of one matrix; y of every expert's rows; or the
+// quantised h = silu(gate) up of every expert's rows.
+enum Mode { kDense = 0, kGrouped = 1, kGated = 2 };
+
+template <int FMT, int NT, int MODE>
 struct Shape {
+  static constexpr int kW = MODE == kGated ? 2 : 1;                      // weight tiles per slot
   static constexpr int kTiles = kChunk / (FMT == HQ_FP4_NV ? 64 : 128);  // scale tiles per chunk
-  static constexpr int kSfA = kTiles * 512;
+  static constexpr int kSf = kTiles * 512;                               // one row tile's scales
   static constexpr int kRowTiles = NT > 128 ? NT / 128 : 1;              // token scale tiles
-  static constexpr int kSfB = kRowTiles * kTiles * 512;
   static constexpr int kABytes = NT * kChunk / 2;
-  static constexpr int kSlot = kWBytes + kABytes + kSfA + kSfB;
-  static constexpr int kAccs = NT <= 128 ? 2 : 1;
-  static constexpr int kSfCols = kTiles * 4 * (1 + kRowTiles);           // one slot's scales
+  static constexpr int kSfOff = kW * kWBytes + kABytes;                  // scales: weights', then tokens'
+  static constexpr int kSlot = kSfOff + (kW + kRowTiles) * kSf;
+  static constexpr int kAccs = kW * NT <= 128 ? 2 : 1;                   // accumulator sets
+  static constexpr int kSfCols = kTiles * 4 * (kW + kRowTiles);          // one slot's scales
   static constexpr int kSfSets = 2;
-  static constexpr int kColsNeeded = kAccs * NT + kSfSets * kSfCols;
+  static constexpr int kColsNeeded = kAccs * kW * NT + kSfSets * kSfCols;
   static constexpr int kCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
-  static constexpr int kEpiWarps = NT > 128 ? 8 : 4;
+  static constexpr int kEpiWarps = kW * NT > 128 ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
-  static constexpr int kStages = NT <= 64 ? 4 : NT <= 128 ? 5 : 4;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kSlot + 512;
+  static constexpr int kStages = kSlot <= 32 * 1024 ? 4 : kSlot <= 40 * 1024 ? 5 : kSlot <= 50 * 1024 ? 4 : MODE == kGated ? 3 : 4;
+  static constexpr int kTurn = MODE == kGated ? kEpiWarps * 16 * kTurnRow * 4 : 0;  // epilogue transposes
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kSlot + kTurn + 512;
   static_assert(kColsNeeded <= 512, "tensor memory");
   static_assert(kSlot % 1024 == 0, "swizzle atoms");
 };
@@ -135,6 +144,14 @@ struct GemmArgs {
   const int32_t* offsets;
   const int32_t* counts;
   int E, n_wts;
+  // gated: the second (up) matrix, and where the quantised h goes
+  const uint8_t* wsf2;
+  const float* wts2;
+  int n_wts2;
+  const float* hts;
+  uint8_t* h_codes;
+  uint8_t* h_scales;
+  int h_kb;
   int early;           // the weights may be read before the preceding kernel ends
 };
 
@@ -148,52 +165,43 @@ struct Item {
 
 template <int NT, bool GROUPED>
 struct Walk {
-  int u, end, step, tile0;
-  // grouped
-  int e, left, first;  // current expert, its first tile's index
-  __device__ __forceinline__ void start(const GemmArgs& a) {
-    if constexpr (GROUPED) {
+  int u, end, step;
+  const int* first;  // grouped: [E + 1] tiles before each expert
+  __device__ __forceinline__ Walk(const GemmArgs& a, const int* tiles_before) : first(tiles_before) {
+    step = gridDim.x;
+    if (GROUPED || a.units == 0) {
       u = blockIdx.x;
-      step = gridDim.x;
-      e = 0;
-      first = 0;
-    } else if (a.units > 0) {
+      end = GROUPED ? first[a.E] : a.mt * a.nt;
+    } else {
       u = static_cast<int>(static_cast<long>(a.units) * blockIdx.x / gridDim.x);
       end = static_cast<int>(static_cast<long>(a.units) * (blockIdx.x + 1) / gridDim.x);
-    } else {
-      u = blockIdx.x;
-      end = a.mt * a.nt;
-      step = gridDim.x;
     }
   }
-  // The next item; false at the end.  n tiles fastest: CTAs that run together
-  // share weight tiles in L2.
+  // The next item; false at the end.
   __device__ __forceinline__ bool next(const GemmArgs& a, Item& it) {
+    if (u >= end) return false;
+    it.c0 = 0;
+    it.c1 = a.C;
     if constexpr (GROUPED) {
-      while (e < a.E) {
-        const int cnt = __ldg(a.counts + e);
-        const int tiles = (cnt + NT - 1) / NT * a.mt;
-        if (u < first + tiles) {
-          const int t = u - first, nti = t / a.mt, mi = t - nti * a.mt;
-          it.m0 = mi * kM;
-          it.n0 = __ldg(a.offsets + e) + nti * NT;
-          it.n_valid = min(NT, cnt - nti * NT);
-          it.w_row = e * a.M + it.m0;
-          it.e = e;
-          it.c0 = 0;
-          it.c1 = a.C;
-          u += step;
-          return true;
+      int e = 0, n = a.E;  // the expert whose tiles include u: first[e] <= u < first[e + 1]
+      while (n > 1) {
+        const int h = n >> 1;
+        if (first[e + h] <= u) {
+          e += h;
+          n -= h;
+        } else {
+          n = h;
         }
-        first += tiles;
-        ++e;
       }
-      return false;
+      const int t = u - first[e], ni = t / a.mt, mi = t - ni * a.mt;
+      it.m0 = mi * kM;
+      it.n0 = __ldg(a.offsets + e) + ni * NT;
+      it.n_valid = min(NT, __ldg(a.counts + e) - ni * NT);
+      it.w_row = e * a.M + it.m0;
+      it.e = e;
+      u += step;
     } else {
-      if (u >= end) return false;
       int tile = u;
-      it.c0 = 0;
-      it.c1 = a.C;
       if (a.units > 0) {
         tile = u / a.C;
         it.c0 = u - tile * a.C;
@@ -202,16 +210,40 @@ struct Walk {
       } else {
         u += step;
       }
+      // token tiles fastest: CTAs that run together share weight tiles in L2
       const int mi = tile / a.nt, ni = tile - mi * a.nt;
       it.m0 = mi * kM;
       it.n0 = ni * NT;
       it.n_valid = min(NT, a.N - it.n0);
       it.w_row = it.m0;
       it.e = 0;
-      return true;
     }
+    return true;
   }
 };
+
+// Tiles before each expert, [E + 1], by the whole CTA.
+template <int NT>
+__device__ __forceinline__ void count_tiles(const GemmArgs& a, int* first) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int carry = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int n = e < a.E ? (__ldg(a.counts + e) + NT - 1) / NT * a.mt : 0;
+      int s = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(~0u, s, o);
+        if (lane >= o) s += v;
+      }
+      if (e < a.E) first[e] = carry + s - n;
+      carry += __shfl_sync(~0u, s, 31);
+    }
+    if (lane == 0) first[a.E] = carry;
+  }
+  __syncthreads();
+}
 
 template <typename T>
 __device__ __forceinline__ void put(void* y, size_t i, float v) {
@@ -220,21 +252,24 @@ __device__ __forceinline__ void put(void* y, size_t i, float v) {
 
 // ------------------------------------------------------------------ kernel
 
-template <int FMT, int NT, bool GROUPED>
-__global__ void __launch_bounds__(Shape<FMT, NT>::kThreads, 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
-                const GemmArgs a) {
-  using S = Shape<FMT, NT>;
+template <int FMT, int NT, int MODE>
+__global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wmap2,
+                const __grid_constant__ CUtensorMap amap, const GemmArgs a) {
+  using S = Shape<FMT, NT, MODE>;
+  constexpr bool GROUPED = MODE != kDense;
   constexpr int ST = S::kStages;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + ST * S::kSlot);
+  float* turn_buf = reinterpret_cast<float*>(ring + ST * S::kSlot);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + ST * S::kSlot + S::kTurn);
   uint64_t* empty = full + ST;
   uint64_t* dfull = empty + ST;
   uint64_t* dempty = dfull + S::kAccs;
   uint64_t* epi = dempty + S::kAccs;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(epi + 1);
   uint32_t* flag = tslot + 1;
+  __shared__ int first[GROUPED ? kMaxGroups + 1 : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -248,6 +283,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT>::kThreads, 1)
     mbar_init(epi, S::kEpiWarps);
     fence_mbar_init();
     prefetch_tensormap(&wmap);
+    if (MODE == kGated) prefetch_tensormap(&wmap2);
     prefetch_tensormap(&amap);
   }
   if (warp == 1) {
@@ -258,15 +294,18 @@ __global__ void __launch_bounds__(Shape<FMT, NT>::kThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tslot;
-  const uint32_t sf_cols = tmem + S::kAccs * NT;
+  const uint32_t sf_cols = tmem + S::kAccs * S::kW * NT;
+  if constexpr (GROUPED) {
+    pdl_wait();  // the segments come from the sort
+    count_tiles<NT>(a, first);
+  }
   bool ok = true;
 
   if (warp == 0) {
     if (lane == 0) {
       const bool early = !GROUPED && a.early != 0;
-      if (!early) pdl_wait();
-      Walk<NT, GROUPED> w;
-      w.start(a);
+      if (!GROUPED && !early) pdl_wait();
+      Walk<NT, GROUPED> w(a, first);
       Item it;
       int slot = 0, turn = 0;
       // With early weights: the first ring of weight copies goes out before the
@@ -278,7 +317,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT>::kThreads, 1)
         tiles = min(S::kTiles, a.wkb - c * S::kTiles);
         row_tiles = min(S::kRowTiles, a.a_row_tiles - (t.n0 >> 7));
         a_rows = GROUPED ? (t.n_valid + 15) / 16 * 16 : NT;
-        return static_cast<uint32_t>(kWBytes + a_rows * 128 + tiles * 512 * (1 + row_tiles));
+        return static_cast<uint32_t>(S::kW * kWBytes + a_rows * 128 + tiles * 512 * (S::kW + row_tiles));
       };
       auto weights = [&](const Item& t, int c, int s) {
         int tiles, row_tiles, a_rows;
@@ -286,8 +325,12 @@ __global__ void __launch_bounds__(Shape<FMT, NT>::kThreads, 1)
         uint8_t* p = ring + s * S::kSlot;
         mbar_arrive_expect_tx(full + s, bytes);
         tma_load_2d(p, &wmap, c * (kChunk / 2), t.w_row, full + s);
-        bulk_g2s(p + kWBytes + S::kABytes, a.wsf + (static_cast<size_t>(t.w_row >> 7) * a.wkb + c * S::kTiles) * 512,
-                 tiles * 512, full + s);
+        const size_t sf = (static_cast<size_t>(t.w_row >> 7) * a.wkb + c * S::kTiles) * 512;
+        bulk_g2s(p + S::kSfOff, a.wsf + sf, tiles * 512, full + s);
+        if constexpr (MODE == kGated) {
+          tma_load_2d(p + kWBytes, &wmap2, c * (kChunk / 2), t.w_row, full + s);
+          bulk_g2s(p + S::kSfOff + S::kSf, a.wsf2 + sf, tiles * 512, full + s);
+        }
       };
       auto tokens = [&](const Item& t, int c, int s) {
         int tiles, row_tiles, a_rows;
@@ -295,13 +338,13 @@ __global__ void __launch_bounds__(Shape<FMT, NT>::kThreads, 1)
         uint8_t* p = ring + s * S::kSlot;
         if constexpr (GROUPED) {
           for (int r = 0; r < a_rows; r += 16) {
-            tma_load_2d(p + kWBytes + r * 128, &amap, c * (kChunk / 2), t.n0 + r, full + s);
+            tma_load_2d(p + S::kW * kWBytes + r * 128, &amap, c * (kChunk / 2), t.n0 + r, full + s);
           }
         } else {
-          tma_load_2d(p + kWBytes, &amap, c * (kChunk / 2), t.n0, full + s);
+          tma_load_2d(p + S::kW * kWBytes, &amap, c * (kChunk / 2), t.n0, full + s);
         }
         for (int r = 0; r < row_tiles; ++r) {
-          bulk_g2s(p + kWBytes + S::kABytes + S::kSfA + r * S::kSfA,
+          bulk_g2s(p + S::kSfOff + (S::kW + r) * S::kSf,
                    a.asf + (static_cast<size_t>((t.n0 >> 7) + r) * a.wkb + c * S::kTiles) * 512, tiles * 512,
                    full + s);
         }
@@ -335,13 +378,11 @@ __global__ void __launch_bounds__(Shape<FMT, NT>::kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      if constexpr (GROUPED) pdl_wait();  // it reads the segments
-      Walk<NT, GROUPED> w;
-      w.start(a);
+      Walk<NT, GROUPED> w(a, first);
       Item it;
       int slot = 0, par = 0, set = 0, acc = 0, accn = 0;
       while (ok && w.next(a, it)) {
-        const uint32_t d = tmem + acc * NT;
+        const uint32_t d = tmem + acc * S::kW * NT;
         if (accn >= S::kAccs && !mbar_wait(dempty + acc, (accn / S::kAccs - 1) & 1)) {
           ok = false;
           break;
@@ -355,24 +396,30 @@ __global__ void __launch_bounds__(Shape<FMT, NT>::kThreads, 1)
           }
           tc::tc_fence_after();
           const uint32_t p = smem_u32(ring + slot * S::kSlot);
-          const uint32_t sfa = sf_cols + set * S::kSfCols, sfb = sfa + S::kTiles * 4;
-          const uint32_t sp = p + kWBytes + S::kABytes;
+          const uint32_t sfa = sf_cols + set * S::kSfCols, sfb = sfa + S::kW * S::kTiles * 4;
+          const uint32_t sp = p + S::kSfOff;
 #pragma unroll
           for (int t = 0; t < S::kTiles; ++t) {
-            tc_copy_scales(sfa + 4 * t, sp + 512 * t);
+#pragma unroll
+            for (int i = 0; i < S::kW; ++i) tc_copy_scales(sfa + 4 * (i * S::kTiles + t), sp + i * S::kSf + 512 * t);
 #pragma unroll
             for (int r = 0; r < S::kRowTiles; ++r) {
-              tc_copy_scales(sfb + 4 * (t * S::kRowTiles + r), sp + S::kSfA * (1 + r) + 512 * t);
+              tc_copy_scales(sfb + 4 * (t * S::kRowTiles + r), sp + S::kSf * (S::kW + r) + 512 * t);
             }
           }
-          const uint64_t da = desc_sw128(p), db = desc_sw128(p + kWBytes);
+          const uint64_t db = desc_sw128(p + S::kW * kWBytes);
           // the tokens' rows within their scale tile: 0 or 64 (two columns)
           const uint32_t half = NT < 128 ? ((it.n0 & 127) >> 5) : 0;
           const int steps = min(4, a.k_steps - 4 * c);
-          for (int s = 0; s < steps; ++s) {
-            const int t = FMT == HQ_FP4_NV ? s : s >> 1, id = FMT == HQ_FP4_NV ? 0 : 2 * (s & 1);
-            tc_mma_scaled<FMT>(d, da + 2 * s, db + 2 * s, idesc_fp4(FMT, n_mma, id), sfa + 4 * t,
-                               sfb + 4 * t * S::kRowTiles + half, (c > it.c0 || s > 0) ? 1u : 0u);
+#pragma unroll
+          for (int i = 0; i < S::kW; ++i) {
+            const uint64_t da = desc_sw128(p + i * kWBytes);
+            for (int s = 0; s < steps; ++s) {
+              const int t = FMT == HQ_FP4_NV ? s : s >> 1, id = FMT == HQ_FP4_NV ? 0 : 2 * (s & 1);
+              tc_mma_scaled<FMT>(d + i * NT, da + 2 * s, db + 2 * s, idesc_fp4(FMT, n_mma, id),
+                                 sfa + 4 * (i * S::kTiles + t), sfb + 4 * t * S::kRowTiles + half,
+                                 (c > it.c0 || s > 0) ? 1u : 0u);
+            }
           }
           tc::tc_commit(empty + slot);
           set ^= 1;
@@ -388,14 +435,13 @@ __global__ void __launch_bounds__(Shape<FMT, NT>::kThreads, 1)
       }
     }
   } else {
-    pdl_wait();
+    if constexpr (!GROUPED) pdl_wait();
     const int ew = warp - 2, quarter = warp & 3;
     constexpr int kParts = S::kEpiWarps / 4;  // warps that share a lane quarter split the columns
     const int col0 = (ew >> 2) * (NT / kParts), col1 = col0 + NT / kParts;
     const int mrow = quarter * 32 + lane;
     const float ats = a.ats != nullptr ? __ldg(a.ats) : 1.f;
-    Walk<NT, GROUPED> w;
-    w.start(a);
+    Walk<NT, GROUPED> w(a, first);
     Item it;
     int acc = 0, accn = 0, epar = 0;
     auto meet = [&]() {  // all epilogue warps, bounded
@@ -411,11 +457,57 @@ __global__ void __launch_bounds__(Shape<FMT, NT>::kThreads, 1)
         break;
       }
       tc::tc_fence_after();
-      const uint32_t d = tmem + acc * NT + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t d = tmem + acc * S::kW * NT + (static_cast<uint32_t>(quarter * 32) << 16);
       const float alpha = (a.wts != nullptr ? __ldg(a.wts + (a.n_wts > 1 ? it.e : 0)) : 1.f) * ats;
       const bool whole = it.c0 == 0 && it.c1 == a.C;
       const int m = it.m0 + mrow;
-      if (whole) {
+      if constexpr (MODE == kGated) {
+        // 16 tokens at a time: h of this lane's feature, a transpose through
+        // shared memory, then 16 features of one token per lane
+        const float alpha2 = (a.wts2 != nullptr ? __ldg(a.wts2 + (a.n_wts2 > 1 ? it.e : 0)) : 1.f) * ats;
+        const float hts = a.hts != nullptr ? __ldg(a.hts) : 1.f;
+        float* buf = turn_buf + ew * 16 * kTurnRow;
+        for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
+          uint32_t g[16], u[16];
+          tc::tc_ld16(d + c, g);
+          tc::tc_ld16(d + NT + c, u);
+          tc::tc_wait_ld();
+          tc::tc_tie16(g);
+          tc::tc_tie16(u);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = __uint_as_float(g[i]) * alpha;
+            buf[i * kTurnRow + lane] = __fdividef(x, 1.f + __expf(-x)) * (__uint_as_float(u[i]) * alpha2);
+          }
+          __syncwarp();
+          const int tok = lane & 15, part = lane >> 4;
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 f = *reinterpret_cast<const float4*>(buf + tok * kTurnRow + part * 16 + 4 * i);
+            v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+          }
+          const Packed16 p = pack16<FMT>(v, hts, 16);
+          const uint32_t other = __shfl_xor_sync(~0u, p.byte, 16);
+          if (c + tok < it.n_valid) {
+            const long row = it.n0 + c + tok;
+            const int f0 = it.m0 + quarter * 32;  // the warp's first feature
+            *reinterpret_cast<uint2*>(a.h_codes + row * (a.M / 2) + (f0 + part * 16) / 2) = p.codes;
+            if (part == 0) {
+              if constexpr (FMT == HQ_FP4_NV) {
+                uint8_t* s = a.h_scales + scale_cell(row, f0 >> 6, a.h_kb) + (quarter & 1) * 2;
+                *reinterpret_cast<uint16_t*>(s) = static_cast<uint16_t>(p.byte | other << 8);
+              } else {
+                a.h_scales[scale_cell(row, f0 >> 7, a.h_kb) + quarter] = static_cast<uint8_t>(p.byte);
+              }
+            }
+          }
+          __syncwarp();
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dempty + acc);
+      } else if (whole) {
         for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
           uint32_t v[16];
           tc::tc_ld16(d + c, v);
@@ -437,7 +529,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT>::kThreads, 1)
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(dempty + acc);
-      } else if constexpr (!GROUPED) {
+      } else if constexpr (MODE == kDense) {
         // a tile shared by CTAs i0 .. i1: the units [t C, t C + C)
         const int t = (it.m0 / kM) * a.nt + it.n0 / NT;
         const long first = static_cast<long>(t) * a.C, last = first + a.C - 1;
@@ -542,22 +634,30 @@ Plan plan_of(int M, int N, int K) {
   return p;
 }
 
-template <int FMT, int NT, bool GROUPED>
-cudaError_t gemm_launch(const CUtensorMap& wmap, const CUtensorMap& amap, const GemmArgs& a, int grid,
-                        cudaStream_t st) {
-  using S = Shape<FMT, NT>;
-  return launch_pdl(gemm_kernel<FMT, NT, GROUPED>, dim3(grid), dim3(S::kThreads), S::kSmem, st, true, wmap, amap, a);
+template <int FMT, int NT, int MODE>
+cudaError_t gemm_launch(const CUtensorMap& wmap, const CUtensorMap& wmap2, const CUtensorMap& amap,
+                        const GemmArgs& a, int grid, cudaStream_t st) {
+  using S = Shape<FMT, NT, MODE>;
+  return launch_pdl(gemm_kernel<FMT, NT, MODE>, dim3(grid), dim3(S::kThreads), S::kSmem, st, true, wmap, wmap2, amap,
+                    a);
 }
 
 template <int FMT>
 cudaError_t dense_launch(int nt, const CUtensorMap& wmap, const CUtensorMap& amap, const GemmArgs& a, int grid,
                          cudaStream_t st) {
   switch (nt) {
-    case 32: return gemm_launch<FMT, 32, false>(wmap, amap, a, grid, st);
-    case 64: return gemm_launch<FMT, 64, false>(wmap, amap, a, grid, st);
-    case 128: return gemm_launch<FMT, 128, false>(wmap, amap, a, grid, st);
-    default: return gemm_launch<FMT, 256, false>(wmap, amap, a, grid, st);
+    case 32: return gemm_launch<FMT, 32, kDense>(wmap, wmap, amap, a, grid, st);
+    case 64: return gemm_launch<FMT, 64, kDense>(wmap, wmap, amap, a, grid, st);
+    case 128: return gemm_launch<FMT, 128, kDense>(wmap, wmap, amap, a, grid, st);
+    default: return gemm_launch<FMT, 256, kDense>(wmap, wmap, amap, a, grid, st);
   }
+}
+
+template <int FMT, int MODE>
+cudaError_t group_launch(int nt, const CUtensorMap& wmap, const CUtensorMap& wmap2, const CUtensorMap& amap,
+                         const GemmArgs& a, int grid, cudaStream_t st) {
+  return nt == 64 ? gemm_launch<FMT, 64, MODE>(wmap, wmap2, amap, a, grid, st)
+                  : gemm_launch<FMT, 128, MODE>(wmap, wmap2, amap, a, grid, st);
 }
 
 cudaError_t code_map(CUtensorMap* map, const uint8_t* codes, long rows, int K, int box_rows) {
@@ -618,6 +718,137 @@ hq_status check_product(const hq_fp4_matrix* w, int N, const void* y, hq_dtype y
 
 bool bad_workspace(const void* ws, size_t bytes, size_t need) {
   return ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) != 0 || bytes < need;
+}
+
+// ------------------------------------------------------------------ experts
+
+// Sizes of an expert layer: hidden H, intermediate I, and the rows that hold
+// every routing (segments start at whole scale tiles).
+struct Layer {
+  int E, H, I, T, k, fmt;
+  long rows;
+};
+
+// Workspace: [status, counters] [sort] [pos] [offsets, counts] [tokens' codes
+// and scales by expert row] [h's codes and scales] [d, the experts' outputs].
+// d has y's type if that is 16 bits (its rounding, half an ulp of each
+// expert's share, is of the size of y's own) and halves the traffic of the two
+// largest passes; fp32 for fp32 y.
+struct LayerWs {
+  size_t sort, pos, ends, xc, xs, hc, hs, d, bytes;
+};
+
+LayerWs layer_ws(const Layer& l, hq_dtype yd) {
+  LayerWs w{};
+  size_t at = kStatusBytes + kCounterBytes;
+  auto take = [&](size_t n) {
+    const size_t a = at;
+    at += align256(n);
+    return a;
+  };
+  const long pairs = static_cast<long>(l.T) * l.k;
+  w.sort = take(route::sort_workspace_bytes(pairs, l.E));
+  w.pos = take(pairs * 4);
+  w.ends = take((2 * static_cast<size_t>(l.E) + 1) * 4);
+  w.xc = take(static_cast<size_t>(l.rows) * (l.H / 2));
+  w.xs = take(scale_bytes(l.fmt, l.rows, l.H));
+  w.hc = take(static_cast<size_t>(l.rows) * (l.I / 2));
+  w.hs = take(scale_bytes(l.fmt, l.rows, l.I));
+  w.d = take(static_cast<size_t>(l.rows) * l.H * (yd == HQ_F32 ? 4 : 2));
+  w.bytes = at;
+  return w;
+}
+
+hq_status check_layer(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, const hq_fp4_matrix* down, int E, int T,
+                      int k, Layer& l) {
+  for (const hq_fp4_matrix* m : {gate, up, down}) {
+    const hq_status ok = check_matrix(m);
+    if (ok != HQ_OK) return ok;
+  }
+  if (E < 1 || T < 0 || k < 1) return HQ_ERR_INVALID_ARG;
+  if (gate->format != up->format || gate->format != down->format || gate->rows != up->rows || gate->K != up->K ||
+      gate->rows % E != 0 || down->rows % E != 0 || gate->rows / E != down->K || down->rows / E != gate->K) {
+    return HQ_ERR_INVALID_ARG;
+  }
+  l = Layer{E, gate->K, down->K, T, k, gate->format, 0};
+  if (l.H < 128 || l.I < 128) return HQ_ERR_UNSUPPORTED;
+  if (E > kMaxGroups || k > 32 || l.H % 128 != 0 || l.I % 128 != 0 || T > (1 << 20)) return HQ_ERR_UNSUPPORTED;
+  for (const hq_fp4_matrix* m : {gate, up, down}) {
+    if (m->tensor_scale != nullptr && m->n_tensor_scales != 1 && m->n_tensor_scales != E) return HQ_ERR_INVALID_ARG;
+  }
+  const long pairs = static_cast<long>(T) * k;
+  if (!route::sort_supported(pairs, E, kM)) return HQ_ERR_UNSUPPORTED;
+  l.rows = (pairs + std::min<long>(E, pairs) * (kM - 1) + kM - 1) / kM * kM;
+  return HQ_OK;
+}
+
+cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, const hq_fp4_matrix* down,
+                           const Layer& l, const void* x, hq_dtype xd, size_t ldx, const int32_t* ids,
+                           const float* topk_w, const float* x_scale, const float* h_scale, void* y, hq_dtype yd,
+                           uint8_t* ws, cudaStream_t st) {
+  const LayerWs o = layer_ws(l, yd);
+  int32_t* pos = reinterpret_cast<int32_t*>(ws + o.pos);
+  int32_t* offsets = reinterpret_cast<int32_t*>(ws + o.ends);
+  int32_t* counts = offsets + l.E + 1;
+  const int rows = static_cast<int>(l.rows);
+  cudaError_t e = route::launch_sort(ids, l.T * l.k, l.E, kM, pos, offsets, counts, ws + o.sort, st);
+  if (e != cudaSuccess) return e;
+  e = launch_quantize(l.fmt, xd, x, ldx, l.T, l.H, x_scale, ws + o.xc, ws + o.xs, nullptr, pos, l.k, rows, st);
+  if (e != cudaSuccess) return e;
+  const int nt = static_cast<long>(l.T) * l.k > 48l * l.E ? 128 : 64;
+  const int grid = std::min(sm_count(), kMaxGrid);
+  CUtensorMap wmap, wmap2, amap;
+  GemmArgs a{};
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.offsets = offsets;
+  a.counts = counts;
+  a.E = l.E;
+  a.a_row_tiles = rows / kM;
+
+  if ((e = code_map(&wmap, gate->codes, gate->rows, l.H, kM)) != cudaSuccess) return e;
+  if ((e = code_map(&wmap2, up->codes, up->rows, l.H, kM)) != cudaSuccess) return e;
+  if ((e = code_map(&amap, ws + o.xc, l.rows, l.H, 16)) != cudaSuccess) return e;
+  a.wsf = gate->scales;
+  a.wts = gate->tensor_scale;
+  a.n_wts = gate->n_tensor_scales;
+  a.wsf2 = up->scales;
+  a.wts2 = up->tensor_scale;
+  a.n_wts2 = up->n_tensor_scales;
+  a.asf = ws + o.xs;
+  a.ats = x_scale;
+  a.wkb = scale_tiles(l.fmt, l.H);
+  a.M = l.I;
+  a.mt = l.I / kM;
+  a.C = (l.H + kChunk - 1) / kChunk;
+  a.k_steps = l.H / 64;
+  a.hts = h_scale;
+  a.h_codes = ws + o.hc;
+  a.h_scales = ws + o.hs;
+  a.h_kb = scale_tiles(l.fmt, l.I);
+  e = l.fmt == HQ_FP4_NV ? group_launch<HQ_FP4_NV, kGated>(nt, wmap, wmap2, amap, a, grid, st)
+                         : group_launch<HQ_FP4_MX, kGated>(nt, wmap, wmap2, amap, a, grid, st);
+  if (e != cudaSuccess) return e;
+
+  if ((e = code_map(&wmap, down->codes, down->rows, l.I, kM)) != cudaSuccess) return e;
+  if ((e = code_map(&amap, ws + o.hc, l.rows, l.I, 16)) != cudaSuccess) return e;
+  a.wsf = down->scales;
+  a.wts = down->tensor_scale;
+  a.n_wts = down->n_tensor_scales;
+  a.asf = ws + o.hs;
+  a.ats = h_scale;
+  a.wkb = a.h_kb;
+  a.M = l.H;
+  a.mt = l.H / kM;
+  a.C = (l.I + kChunk - 1) / kChunk;
+  a.k_steps = l.I / 64;
+  const hq_dtype dd = yd;
+  a.y = ws + o.d;
+  a.y_dtype = dd;
+  a.ldy = l.H;
+  e = l.fmt == HQ_FP4_NV ? group_launch<HQ_FP4_NV, kGrouped>(nt, wmap, wmap, amap, a, grid, st)
+                         : group_launch<HQ_FP4_MX, kGrouped>(nt, wmap, wmap, amap, a, grid, st);
+  if (e != cudaSuccess) return e;
+  return route::launch_combine(dd, yd, ws + o.d, pos, topk_w, y, l.T, l.k, l.H, rows, st);
 }
 
 size_t packed_bytes(int fmt, long rows, int K) {
@@ -685,5 +916,39 @@ hq_status hq_fp4_linear(const hq_fp4_matrix* w, const void* x, hq_dtype x_dtype,
 }
 
 int hq_fp4_linear_launches(void) { return 2; }
+
+size_t hq_fp4_experts_workspace_size(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, const hq_fp4_matrix* down,
+                                     int n_experts, int T, int k, hq_dtype y_dtype) {
+  fp4::Layer l{};
+  if (y_dtype < HQ_F16 || y_dtype > HQ_F32 || fp4::check_layer(gate, up, down, n_experts, T, k, l) != HQ_OK) return 0;
+  return fp4::layer_ws(l, y_dtype).bytes;
+}
+
+hq_status hq_fp4_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, const hq_fp4_matrix* down,
+                         int n_experts, const void* x, hq_dtype x_dtype, size_t ldx, int T, const int32_t* topk_ids,
+                         const float* topk_w, int k, const float* x_scale, const float* h_scale, void* y,
+                         hq_dtype y_dtype, void* workspace, size_t ws_bytes, hq_stream_t stream) {
+  fp4::Layer l{};
+  const hq_status ok = fp4::check_layer(gate, up, down, n_experts, T, k, l);
+  if (ok != HQ_OK) return ok;
+  if (y_dtype < HQ_F16 || y_dtype > HQ_F32) return HQ_ERR_INVALID_ARG;
+  for (const float* s : {x_scale, h_scale}) {
+    if (s != nullptr && (l.fmt != HQ_FP4_NV || (reinterpret_cast<uintptr_t>(s) & 3) != 0)) return HQ_ERR_INVALID_ARG;
+  }
+  if (T == 0) return HQ_OK;
+  const hq_status rows_ok = fp4::check_rows(x, x_dtype, ldx, l.H);
+  if (rows_ok != HQ_OK) return rows_ok;
+  auto bad = [](const void* p, uintptr_t a) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; };
+  if (bad(topk_ids, 4) || bad(topk_w, 4) || bad(y, 16)) return HQ_ERR_INVALID_ARG;
+  if (fp4::bad_workspace(workspace, ws_bytes, fp4::layer_ws(l, y_dtype).bytes)) return HQ_ERR_WORKSPACE;
+  return from_cuda(fp4::launch_experts(gate, up, down, l, x, x_dtype, ldx, topk_ids, topk_w, x_scale, h_scale, y,
+                                       y_dtype, static_cast<uint8_t*>(workspace),
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int hq_fp4_experts_launches(int T, int k) {
+  if (T < 1 || k < 1 || k > 32) return 0;
+  return 4 + route::sort_launches(static_cast<long>(T) * k);
+}
 
 }  // extern "C"

@@ -12,11 +12,11 @@
 // scale and, if asked for, its rounded value.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include <algorithm>
 
 #include "fp4.cuh"
+#include "fp4_quant.cuh"
 #include "hq_common.cuh"
 #include "hq_internal.h"
 #include "hq_io.cuh"
@@ -27,61 +27,6 @@ namespace fp4 {
 namespace {
 
 constexpr int kThreads = 256;
-
-// The block scale of amax: the scale byte and its value times the tensor
-// scale.  In IEEE single precision, as the header defines it.
-template <int FMT>
-__device__ __forceinline__ void block_scale(float amax, float ts, uint32_t& byte, float& eff) {
-  if constexpr (FMT == HQ_FP4_NV) {
-    byte = __nv_cvt_float_to_fp8(__fdiv_rn(amax, __fmul_rn(6.f, ts)), __NV_SATFINITE, __NV_E4M3);
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3);
-    eff = __fmul_rn(__half2float(__half(h)), ts);
-  } else {
-    // floor(log2 amax) - 2, at least -127: the exponent field of a normal
-    // amax less 2 (a subnormal amax gives the smallest scale either way)
-    const int f = static_cast<int>(__float_as_uint(amax) >> 23) - 2;
-    byte = static_cast<uint32_t>(max(f, 0));
-    eff = byte == 0 ? __uint_as_float(1u << 22) : __uint_as_float(byte << 23);
-  }
-}
-
-// x / eff for 16 values.  Where 1 / eff is far from under- and overflow, by
-// Markstein's quotient correction (IBM J. Res. Dev. 34, 1990): with y the
-// correctly rounded 1 / eff, q = x y is within an ulp and q + (x - q eff) y,
-// both steps fused, rounds to the correctly rounded quotient; so ties between
-// codes are met exactly, at 3 operations a value instead of a division.
-__device__ __forceinline__ void quotients(float (&v)[16], float eff) {
-  if (eff >= 0x1p-100f && eff <= 0x1p100f) {
-    const float y = __frcp_rn(eff);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float q = __fmul_rn(v[i], y);
-      v[i] = __fmaf_rn(__fmaf_rn(-q, eff, v[i]), y, q);
-    }
-  } else if (eff > 0.f) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(v[i], eff);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = copysignf(0.f, v[i]);
-  }
-}
-
-// Two values to two E2M1 codes (low nibble first), round to nearest even,
-// saturating.
-__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
-      : "=r"(r)
-      : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ float2 from_e2m1x2(uint32_t b) {
-  uint32_t h;
-  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(b));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 
 template <typename T>
 __device__ __forceinline__ void store16(T* p, const float (&v)[16]) {
@@ -130,37 +75,9 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = 0.f;
   }
-  float amax = 0.f;
-  bool fine = true;  // every value finite
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float m = fabsf(v[i]);
-    amax = fmaxf(amax, m);
-    fine = fine && m < INFINITY;
-  }
-  if constexpr (FMT == HQ_FP4_MX) {
-    amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
-    fine = __shfl_xor_sync(~0u, static_cast<int>(fine), 1) && fine;
-  }
   const float ts = FMT == HQ_FP4_NV && a.ts != nullptr ? __ldg(a.ts) : 1.f;
-  uint32_t byte;
-  float eff;
-  block_scale<FMT>(amax, ts, byte, eff);
-  if (!fine) {  // the format's NaN as the scale, over codes of zero
-    byte = FMT == HQ_FP4_NV ? 0x7Fu : 0xFFu;
-    eff = __uint_as_float(0x7FC00000u);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
-  } else {
-    quotients(v, eff);
-  }
-  if (!live) byte = 0;
-  uint2 code;
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = to_e2m1x2(v[2 * i], v[2 * i + 1]);
-  code.x = w[0] | w[1] << 8 | w[2] << 16 | w[3] << 24;
-  code.y = w[4] | w[5] << 8 | w[6] << 16 | w[7] << 24;
+  const Packed16 p = pack16<FMT>(v, ts, 1);
+  const uint32_t byte = live ? p.byte : 0u;
   // four blocks' scales in one word
   constexpr int S = FMT == HQ_FP4_NV ? 0 : 1;  // log2 of the threads per block
   uint32_t sw = byte << (8 * (c >> S & 3));
@@ -169,14 +86,14 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
   const bool scale_lane = (c & ((4 << S) - 1)) == 0 && c < a.c_pad;
   const int st = c >> (2 + S);  // scale tile along K
   if (a.pos == nullptr) {
-    if (live) *reinterpret_cast<uint2*>(a.codes + row * (a.K / 2) + c * 8) = code;
+    if (live) *reinterpret_cast<uint2*>(a.codes + row * (a.K / 2) + c * 8) = p.codes;
     if (scale_lane && row < a.rows_pad) *reinterpret_cast<uint32_t*>(a.scales + scale_cell(row, st, a.kb)) = sw;
     if (a.values != nullptr && live) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float2 f = from_e2m1x2(w[i]);
-        v[2 * i] = f.x * eff;
-        v[2 * i + 1] = f.y * eff;
+        const float2 f = from_e2m1x2((i < 4 ? p.codes.x : p.codes.y) >> (8 * (i & 3)));
+        v[2 * i] = f.x * p.eff;
+        v[2 * i + 1] = f.y * p.eff;
       }
       store16<T>(static_cast<T*>(a.values) + row * a.K + c * 16, v);
     }
@@ -184,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
     for (int j = 0; j < a.k; ++j) {
       const int r = __ldg(a.pos + row * a.k + j);
       if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.dst_rows)) continue;
-      if (live) *reinterpret_cast<uint2*>(a.codes + static_cast<long>(r) * (a.K / 2) + c * 8) = code;
+      if (live) *reinterpret_cast<uint2*>(a.codes + static_cast<long>(r) * (a.K / 2) + c * 8) = p.codes;
       if (scale_lane) *reinterpret_cast<uint32_t*>(a.scales + scale_cell(r, st, a.kb)) = sw;
     }
   }

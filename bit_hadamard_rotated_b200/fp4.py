@@ -213,4 +213,65 @@ class Fp4Linear:
             check(lib().hq_check_status(_ptr(self._ws), _raw_stream(stream, self._ws.device.index)), "device status")
 
 
-__all__ = ["Fp4Matrix", "Fp4Linear", "hq_fp4_tensor_scale", "hq_fp4_quantize", "hq_fp4_matmul", "hq_fp4_linear"]
+class Fp4Experts:
+    """The routed-expert layer on packed weights with its workspace
+    (hq_fp4_experts): gate, up [n_experts * inter rows], down [n_experts *
+    hidden rows].  x_scale, h_scale: tensor scales of the activations and of
+    h ("nv"), or None.  One layer serves one stream at a time."""
+
+    def __init__(self, gate: Fp4Matrix, up: Fp4Matrix, down: Fp4Matrix, n_experts: int,
+                 x_scale: torch.Tensor | None = None, h_scale: torch.Tensor | None = None,
+                 out_dtype: torch.dtype | None = None):
+        dev = gate.codes.device
+        if up.codes.device != dev or down.codes.device != dev:
+            raise ValueError(f"the three matrices must be on one device, {dev}")
+        _need_scale(x_scale, dev)
+        _need_scale(h_scale, dev)
+        self.gate, self.up, self.down, self.n_experts = gate, up, down, int(n_experts)
+        self.x_scale, self.h_scale, self.out_dtype = x_scale, h_scale, out_dtype
+        self.hidden = gate.K
+        self._ws, self._room = None, (0, 0, None)
+        if not self._need(1, 1, torch.float32):
+            raise ValueError("unsupported expert layer: formats, sizes or tensor scales do not fit together")
+
+    def _need(self, T, k, dtype):
+        return int(lib().hq_fp4_experts_workspace_size(self.gate._ref, self.up._ref, self.down._ref, self.n_experts, T, k,
+                                                       _DT[dtype]))
+
+    def __call__(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+        """y [T][hidden] of x [T][hidden], topk_ids int32 [T][k], topk_w fp32 [T][k]."""
+        dev = self.gate.codes.device
+        x = _rows_in(x, self.hidden)
+        T = x.shape[0]
+        if topk_ids.dtype != torch.int32 or topk_w.dtype != torch.float32 or topk_ids.dim() != 2 \
+                or topk_ids.shape[0] != T or topk_w.shape != topk_ids.shape:
+            raise ValueError(f"topk_ids and topk_w must be int32 and fp32 [{T}][k]")
+        for t in (x, topk_ids, topk_w):
+            if t.device != dev:
+                raise ValueError(f"a tensor is on {t.device}, the weights on {dev}")
+        k = topk_ids.shape[1]
+        ids, w = topk_ids.contiguous(), topk_w.contiguous()
+        with torch.cuda.device(dev):
+            dtype = self.out_dtype or (x.dtype if out is None else out.dtype)
+            if out is None:
+                out = torch.empty((T, self.hidden), dtype=dtype, device=dev)
+            elif out.dtype != dtype or tuple(out.shape) != (T, self.hidden) or not out.is_contiguous() or out.device != dev:
+                raise ValueError(f"out must be contiguous {dtype} [{T}][{self.hidden}] on {dev}")
+            room = self._room
+            if self._ws is None or T > room[0] or k != room[1] or dtype != room[2]:
+                self._ws, self._room = _workspace(None, self._need(T, k, dtype), dev), (T, k, dtype)
+            st = lib().hq_fp4_experts(self.gate._ref, self.up._ref, self.down._ref, self.n_experts, x.data_ptr(),
+                                      _DT[x.dtype], max(x.stride(0), self.hidden), T, ids.data_ptr(), w.data_ptr(), k,
+                                      _ptr(self.x_scale), _ptr(self.h_scale), out.data_ptr(), _DT[dtype],
+                                      self._ws.data_ptr(), self._ws.numel(), _raw_stream(stream, dev.index))
+            if st:
+                check(st, "hq_fp4_experts")
+        return out
+
+    def check_status(self, stream=None):
+        if self._ws is not None:
+            check(lib().hq_check_status(_ptr(self._ws), _raw_stream(stream, self._ws.device.index)), "device status")
+
+
+__all__ = ["Fp4Experts", "Fp4Matrix", "Fp4Linear", "hq_fp4_tensor_scale", "hq_fp4_quantize", "hq_fp4_matmul", "hq_fp4_linear"]

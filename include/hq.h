@@ -457,6 +457,37 @@ hq_status hq_fp4_linear(const hq_fp4_matrix* w, const void* x, hq_dtype x_dtype,
 /* Kernels one hq_fp4_linear call enqueues. */
 int hq_fp4_linear_launches(void);
 
+/* Bytes of workspace hq_fp4_experts needs (0 on a bad argument); enough for
+ * fewer tokens too. */
+size_t hq_fp4_experts_workspace_size(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, const hq_fp4_matrix* down,
+                                     int n_experts, int T, int k, hq_dtype y_dtype);
+
+/*
+ * hq_fp4_experts -- the routed-expert layer on packed 4-bit weights, for any
+ * number of tokens; the steps are those of hq_moe_sort, hq_fp4_quantize,
+ * hq_fp4_matmul and hq_moe_combine, without host synchronisation:
+ *   a    = q(x_t)                                 quantised once per token
+ *   g, u = W_gate^e a,  W_up^e a                  for e = topk_ids[t][j], fp32
+ *   h    = q(g / (1 + exp(-g)) * u)
+ *   d    = W_down^e h                             rounded to y_dtype
+ *   y_t  = sum_j topk_w[t][j] d_{t,j}             fp32, slots ascending, rounded
+ * gate, up: [n_experts * inter] rows of K = hidden, down: [n_experts * hidden]
+ * rows of K = inter, each expert's rows in a run; one format; hidden and inter
+ * multiples of 128, n_experts <= 1024, T <= 2^20, k <= 32
+ * (HQ_ERR_UNSUPPORTED otherwise).  tensor_scale: one value, or one per expert.
+ * x: [T][hidden], row stride ldx, as in hq_fp4_quantize; x_scale, h_scale:
+ * tensor scales of the two quantisations (NV; NULL: 1).  Ids outside [0,
+ * n_experts) add nothing (a token without a valid id gets zeros).  y:
+ * [T][hidden], 16-byte aligned.
+ */
+hq_status hq_fp4_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, const hq_fp4_matrix* down,
+                         int n_experts, const void* x, hq_dtype x_dtype, size_t ldx, int T, const int32_t* topk_ids,
+                         const float* topk_w, int k, const float* x_scale, const float* h_scale, void* y,
+                         hq_dtype y_dtype, void* workspace, size_t ws_bytes, hq_stream_t stream);
+
+/* Kernels one hq_fp4_experts call enqueues. */
+int hq_fp4_experts_launches(int T, int k);
+
 /*
  * Tokens sorted by expert and back: the steps that hq_moe_experts takes
  * inside, for callers that run their own products between them.
