@@ -12,12 +12,18 @@
 //
 // One CTA walks a list of (tile, K range) items.  Per 256 values of K it needs
 // 16 KB of weight codes (one TMA box, 128-byte swizzle), the tokens' codes,
-// and the scale tiles (bulk copies: they lie in memory as tcgen05.cp wants
-// them), all on one mbarrier per ring slot.
-//   warp 0   producer: one thread issues the copies
-//   warp 1   one thread moves the slot's scales to tensor memory and issues
-//            the MMAs (K = 64 each); their commit frees the slot
-//   others   epilogue: tensor memory to registers, alpha, one rounding, y
+// and the scale tiles (bulk copies), all on one mbarrier per ring slot.
+//   warp 0     producer: one thread issues the copies
+//   warp 1     one thread issues the MMAs (K = 64 each); their commit frees
+//              the slot
+//   warps 2-5  the slot's scales from shared to tensor memory, one column set
+//              per slot (a scale tile is 16 bytes per lane: one vector load and
+//              a share of a 16-column store)
+//   others     epilogue: tensor memory to registers, alpha, one rounding, y
+// The scales go through registers because tcgen05.cp costs its issuing thread
+// about 55 cycles a tile beside about 115 per MMA (128 at N = 256, the pipe's
+// rate): 12 tiles and 4 MMAs of a 256-token chunk took 1164 cycles from one
+// thread, the MMAs alone 512.
 // Two accumulators where they fit (up to 128 tokens), so the next tile's MMAs
 // run under the epilogue.
 //
@@ -48,14 +54,15 @@ constexpr int kChunk = 256;  // values of K per ring slot (128 bytes a row)
 constexpr int kWBytes = kM * kChunk / 2;
 constexpr int kTurnRow = 36;  // floats per token of an epilogue transpose (32 and padding)
 constexpr int kMaxGroups = 1024;
+constexpr int kSmemMax = 220 * 1024;
 
 // ------------------------------------------------------------------ PTX
 
-// Scale tile (512 bytes) to four tensor-memory columns, in all four lane
-// quarters.
-__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t smem) {
-  const uint64_t desc = tc::smem_desc(smem, 0, 128);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// 8 consecutive 32-bit tensor-memory columns of this thread's lane.
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // D (+)= (A sA) (B sB), K = 64, E2M1, A and B K-major in shared memory.
@@ -111,15 +118,16 @@ struct Shape {
   static constexpr int kSlot = kSfOff + (kW + kRowTiles) * kSf;
   static constexpr int kAccs = kW * NT <= 128 ? 2 : 1;                   // accumulator sets
   static constexpr int kSfCols = kTiles * 4 * (kW + kRowTiles);          // one slot's scales
-  static constexpr int kSfSets = 2;
-  static constexpr int kColsNeeded = kAccs * kW * NT + kSfSets * kSfCols;
-  static constexpr int kCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
   static constexpr int kEpiWarps = kW * NT > 128 ? 8 : 4;
-  static constexpr int kThreads = 64 + 32 * kEpiWarps;
-  static constexpr int kStages = kSlot <= 32 * 1024 ? 4 : kSlot <= 40 * 1024 ? 5 : kSlot <= 50 * 1024 ? 4 : MODE == kGated ? 3 : 4;
+  static constexpr int kThreads = 64 + 128 + 32 * kEpiWarps;
   static constexpr int kTurn = MODE == kGated ? kEpiWarps * 16 * kTurnRow * 4 : 0;  // epilogue transposes
+  static constexpr int kFit = (kSmemMax - kTurn - 2048) / kSlot;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kColsNeeded = kAccs * kW * NT + kStages * kSfCols;
+  static constexpr int kCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kSlot + kTurn + 512;
   static_assert(kColsNeeded <= 512, "tensor memory");
+  static_assert(kSfCols % 8 == 0, "whole stores");
   static_assert(kSlot % 1024 == 0, "swizzle atoms");
 };
 
@@ -245,9 +253,11 @@ __device__ __forceinline__ void count_tiles(const GemmArgs& a, int* first) {
   __syncthreads();
 }
 
-template <typename T>
-__device__ __forceinline__ void put(void* y, size_t i, float v) {
-  static_cast<T*>(y)[i] = from_f32<T>(v);
+// y[i] = v, rounded to y's type.
+__device__ __forceinline__ void store_y(const GemmArgs& a, size_t i, float v) {
+  if (a.y_dtype == HQ_BF16) static_cast<__nv_bfloat16*>(a.y)[i] = __float2bfloat16_rn(v);
+  else if (a.y_dtype == HQ_F16) static_cast<__half*>(a.y)[i] = __float2half_rn(v);
+  else static_cast<float*>(a.y)[i] = v;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -264,7 +274,8 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   float* turn_buf = reinterpret_cast<float*>(ring + ST * S::kSlot);
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + ST * S::kSlot + S::kTurn);
   uint64_t* empty = full + ST;
-  uint64_t* dfull = empty + ST;
+  uint64_t* sfull = empty + ST;
+  uint64_t* dfull = sfull + ST;
   uint64_t* dempty = dfull + S::kAccs;
   uint64_t* epi = dempty + S::kAccs;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(epi + 1);
@@ -275,6 +286,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     for (int i = 0; i < ST; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
+      mbar_init(sfull + i, 4);
     }
     for (int i = 0; i < S::kAccs; ++i) {
       mbar_init(dfull + i, 1);
@@ -380,7 +392,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     if (lane == 0) {
       Walk<NT, GROUPED> w(a, first);
       Item it;
-      int slot = 0, par = 0, set = 0, acc = 0, accn = 0;
+      int slot = 0, par = 0, acc = 0, accn = 0;
       while (ok && w.next(a, it)) {
         const uint32_t d = tmem + acc * S::kW * NT;
         if (accn >= S::kAccs && !mbar_wait(dempty + acc, (accn / S::kAccs - 1) & 1)) {
@@ -390,39 +402,29 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         tc::tc_fence_after();
         const int n_mma = (it.n_valid + 15) / 16 * 16;
         for (int c = it.c0; c < it.c1; ++c) {
-          if (!mbar_wait(full + slot, par)) {
+          if (!mbar_wait(full + slot, par) || !mbar_wait(sfull + slot, par)) {
             ok = false;
             break;
           }
           tc::tc_fence_after();
           const uint32_t p = smem_u32(ring + slot * S::kSlot);
-          const uint32_t sfa = sf_cols + set * S::kSfCols, sfb = sfa + S::kW * S::kTiles * 4;
-          const uint32_t sp = p + S::kSfOff;
-#pragma unroll
-          for (int t = 0; t < S::kTiles; ++t) {
-#pragma unroll
-            for (int i = 0; i < S::kW; ++i) tc_copy_scales(sfa + 4 * (i * S::kTiles + t), sp + i * S::kSf + 512 * t);
-#pragma unroll
-            for (int r = 0; r < S::kRowTiles; ++r) {
-              tc_copy_scales(sfb + 4 * (t * S::kRowTiles + r), sp + S::kSf * (S::kW + r) + 512 * t);
-            }
-          }
+          const uint32_t sfa = sf_cols + slot * S::kSfCols, sfb = sfa + S::kW * S::kTiles * 4;
           const uint64_t db = desc_sw128(p + S::kW * kWBytes);
           // the tokens' rows within their scale tile: 0 or 64 (two columns)
           const uint32_t half = NT < 128 ? ((it.n0 & 127) >> 5) : 0;
           const int steps = min(4, a.k_steps - 4 * c);
 #pragma unroll
-          for (int i = 0; i < S::kW; ++i) {
-            const uint64_t da = desc_sw128(p + i * kWBytes);
-            for (int s = 0; s < steps; ++s) {
+          for (int s = 0; s < 4; ++s) {
+            if (s >= steps) break;
+#pragma unroll
+            for (int i = 0; i < S::kW; ++i) {
               const int t = FMT == HQ_FP4_NV ? s : s >> 1, id = FMT == HQ_FP4_NV ? 0 : 2 * (s & 1);
-              tc_mma_scaled<FMT>(d + i * NT, da + 2 * s, db + 2 * s, idesc_fp4(FMT, n_mma, id),
+              tc_mma_scaled<FMT>(d + i * NT, desc_sw128(p + i * kWBytes) + 2 * s, db + 2 * s, idesc_fp4(FMT, n_mma, id),
                                  sfa + 4 * (i * S::kTiles + t), sfb + 4 * t * S::kRowTiles + half,
                                  (c > it.c0 || s > 0) ? 1u : 0u);
             }
           }
           tc::tc_commit(empty + slot);
-          set ^= 1;
           if (++slot == ST) {
             slot = 0;
             par ^= 1;
@@ -434,9 +436,45 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         acc = accn % S::kAccs;
       }
     }
+  } else if (warp < 6) {
+    const int quarter = warp & 3;
+    Walk<NT, GROUPED> w(a, first);
+    Item it;
+    int slot = 0, par = 0;
+    while (ok && w.next(a, it)) {
+      for (int c = it.c0; c < it.c1; ++c) {
+        if (!__all_sync(~0u, mbar_wait(full + slot, par))) {
+          ok = false;
+          break;
+        }
+        const uint32_t sp = smem_u32(ring + slot * S::kSlot + S::kSfOff) + lane * 16;
+        uint32_t v[S::kSfCols];
+#pragma unroll
+        for (int i = 0; i < S::kSfCols / 4; ++i) {
+          // columns: the weights' tiles, then the tokens', row tiles innermost
+          constexpr int kWTiles = S::kW * S::kTiles;
+          const int j = i - kWTiles;
+          const int at = i < kWTiles ? i * 512 : (S::kW + j % S::kRowTiles) * S::kSf + j / S::kRowTiles * 512;
+          const uint4 u = lds128(sp + at);
+          v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+        }
+        const uint32_t dst = sf_cols + slot * S::kSfCols + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+        for (int i = 0; i < S::kSfCols; i += 8) tc_st8(dst + i, v + i);
+        tc::tc_wait_st();
+        tc::tc_fence_before();
+        fence_proxy_async_smem();  // the reads above come before the slot's next copies
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfull + slot);
+        if (++slot == ST) {
+          slot = 0;
+          par ^= 1;
+        }
+      }
+    }
   } else {
     if constexpr (!GROUPED) pdl_wait();
-    const int ew = warp - 2, quarter = warp & 3;
+    const int ew = warp - 6, quarter = warp & 3;
     constexpr int kParts = S::kEpiWarps / 4;  // warps that share a lane quarter split the columns
     const int col0 = (ew >> 2) * (NT / kParts), col1 = col0 + NT / kParts;
     const int mrow = quarter * 32 + lane;
@@ -517,11 +555,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               if (c + i < it.n_valid) {
-                const size_t o = static_cast<size_t>(it.n0 + c + i) * a.ldy + m;
-                const float f = __uint_as_float(v[i]) * alpha;
-                if (a.y_dtype == HQ_BF16) put<__nv_bfloat16>(a.y, o, f);
-                else if (a.y_dtype == HQ_F16) put<__half>(a.y, o, f);
-                else put<float>(a.y, o, f);
+                store_y(a, static_cast<size_t>(it.n0 + c + i) * a.ldy + m, __uint_as_float(v[i]) * alpha);
               }
             }
           }
@@ -564,17 +598,23 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         }
         if (*reinterpret_cast<volatile uint32_t*>(flag) != 0) {
           __threadfence();
-          for (int c = col0; c < col1 && c < it.n_valid; ++c) {
-            float s = 0.f;
-            for (int i = i0; i <= i1; ++i) {
-              s += __ldcg(a.part + (2 * static_cast<size_t>(i) + (i == i0 ? 1 : 0)) * part_size + c * kM + mrow);
+          for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
+            float f[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] = 0.f;
+            for (int i = i0; i <= i1; ++i) {  // 16 loads in flight
+              const float* p = a.part + (2 * static_cast<size_t>(i) + (i == i0 ? 1 : 0)) * part_size + c * kM + mrow;
+              float v[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = __ldcg(p + j * kM);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) f[j] += v[j];
             }
             if (m < a.M) {
-              const size_t o = static_cast<size_t>(it.n0 + c) * a.ldy + m;
-              const float f = s * alpha;
-              if (a.y_dtype == HQ_BF16) put<__nv_bfloat16>(a.y, o, f);
-              else if (a.y_dtype == HQ_F16) put<__half>(a.y, o, f);
-              else put<float>(a.y, o, f);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (c + j < it.n_valid) store_y(a, static_cast<size_t>(it.n0 + c + j) * a.ldy + m, f[j] * alpha);
+              }
             }
           }
           if (ew == 0 && lane == 0) a.counters[i0] = 0;
