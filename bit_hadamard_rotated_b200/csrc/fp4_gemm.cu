@@ -54,7 +54,7 @@ constexpr int kChunk = 256;  // values of K per ring slot (128 bytes a row)
 constexpr int kWBytes = kM * kChunk / 2;
 constexpr int kTurnRow = 36;  // floats per token of an epilogue transpose (32 and padding)
 constexpr int kMaxGroups = 1024;
-constexpr int kSmemMax = 220 * 1024;
+constexpr int kSmemMax = 218 * 1024;  // dynamic; the experts' segments (12 KB) beside it
 
 // ------------------------------------------------------------------ PTX
 
@@ -118,10 +118,10 @@ struct Shape {
   static constexpr int kSlot = kSfOff + (kW + kRowTiles) * kSf;
   static constexpr int kAccs = kW * NT <= 128 ? 2 : 1;                   // accumulator sets
   static constexpr int kSfCols = kTiles * 4 * (kW + kRowTiles);          // one slot's scales
-  static constexpr int kEpiWarps = kW * NT > 128 ? 8 : 4;
+  static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = 64 + 128 + 32 * kEpiWarps;
   static constexpr int kTurn = MODE == kGated ? kEpiWarps * 16 * kTurnRow * 4 : 0;  // epilogue transposes
-  static constexpr int kFit = (kSmemMax - kTurn - 2048) / kSlot;
+  static constexpr int kFit = (kSmemMax - kTurn - 2048 - (MODE == kDense ? 0 : 4096)) / kSlot;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kColsNeeded = kAccs * kW * NT + kStages * kSfCols;
   static constexpr int kCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
@@ -168,18 +168,36 @@ struct Item {
   int m0, n0, n_valid;  // first weight row in its expert, first token row, token rows
   int w_row;            // first weight row in the matrix
   int e;
-  int c0, c1;
+  int c0, c1;  // chunks of K
 };
 
 template <int NT, bool GROUPED>
 struct Walk {
-  int u, end, step;
-  const int* first;  // grouped: [E + 1] tiles before each expert
-  __device__ __forceinline__ Walk(const GemmArgs& a, const int* tiles_before) : first(tiles_before) {
-    step = gridDim.x;
-    if (GROUPED || a.units == 0) {
+  int u, end;
+  const int* first;  // grouped: [E + 1] tiles before each expert, then [E] segment starts, [E] row counts
+  int e, ni, mi;     // grouped: the next tile
+  __device__ __forceinline__ Walk(const GemmArgs& a, const int* groups) : first(groups) {
+    if constexpr (GROUPED) {
+      // an even run of tiles per CTA, m tiles fastest
+      const long all = first[a.E];
+      u = static_cast<int>(all * blockIdx.x / gridDim.x);
+      end = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
+      e = 0;
+      int n = a.E;  // the expert whose tiles include u: first[e] <= u < first[e + 1]
+      while (n > 1) {
+        const int h = n >> 1;
+        if (first[e + h] <= u) {
+          e += h;
+          n -= h;
+        } else {
+          n = h;
+        }
+      }
+      ni = (u - first[e]) / a.mt;
+      mi = u - first[e] - ni * a.mt;
+    } else if (a.units == 0) {
       u = blockIdx.x;
-      end = GROUPED ? first[a.E] : a.mt * a.nt;
+      end = a.mt * a.nt;
     } else {
       u = static_cast<int>(static_cast<long>(a.units) * blockIdx.x / gridDim.x);
       end = static_cast<int>(static_cast<long>(a.units) * (blockIdx.x + 1) / gridDim.x);
@@ -191,23 +209,22 @@ struct Walk {
     it.c0 = 0;
     it.c1 = a.C;
     if constexpr (GROUPED) {
-      int e = 0, n = a.E;  // the expert whose tiles include u: first[e] <= u < first[e + 1]
-      while (n > 1) {
-        const int h = n >> 1;
-        if (first[e + h] <= u) {
-          e += h;
-          n -= h;
-        } else {
-          n = h;
-        }
+      const int* starts = first + a.E + 1;
+      if (mi == a.mt) {
+        mi = 0;
+        ++ni;
       }
-      const int t = u - first[e], ni = t / a.mt, mi = t - ni * a.mt;
+      while (ni * NT >= starts[a.E + e]) {  // the next expert that has rows
+        ++e;
+        ni = 0;
+      }
       it.m0 = mi * kM;
-      it.n0 = __ldg(a.offsets + e) + ni * NT;
-      it.n_valid = min(NT, __ldg(a.counts + e) - ni * NT);
+      it.n0 = starts[e] + ni * NT;
+      it.n_valid = min(NT, starts[a.E + e] - ni * NT);
       it.w_row = e * a.M + it.m0;
       it.e = e;
-      u += step;
+      ++mi;
+      ++u;
     } else {
       int tile = u;
       if (a.units > 0) {
@@ -216,12 +233,12 @@ struct Walk {
         it.c1 = min(a.C, it.c0 + end - u);
         u += it.c1 - it.c0;
       } else {
-        u += step;
+        u += gridDim.x;
       }
       // token tiles fastest: CTAs that run together share weight tiles in L2
-      const int mi = tile / a.nt, ni = tile - mi * a.nt;
-      it.m0 = mi * kM;
-      it.n0 = ni * NT;
+      const int mi_ = tile / a.nt, ni_ = tile - mi_ * a.nt;
+      it.m0 = mi_ * kM;
+      it.n0 = ni_ * NT;
       it.n_valid = min(NT, a.N - it.n0);
       it.w_row = it.m0;
       it.e = 0;
@@ -230,15 +247,21 @@ struct Walk {
   }
 };
 
-// Tiles before each expert, [E + 1], by the whole CTA.
+// The experts' tiles and segments into shared memory, by the whole CTA.
 template <int NT>
-__device__ __forceinline__ void count_tiles(const GemmArgs& a, int* first) {
+__device__ __forceinline__ void load_groups(const GemmArgs& a, int* first) {
+  int* starts = first + a.E + 1;
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+    starts[e] = __ldg(a.offsets + e);
+    starts[a.E + e] = __ldg(a.counts + e);
+  }
+  __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int carry = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
-      const int n = e < a.E ? (__ldg(a.counts + e) + NT - 1) / NT * a.mt : 0;
+      const int n = e < a.E ? (starts[a.E + e] + NT - 1) / NT * a.mt : 0;
       int s = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -253,11 +276,41 @@ __device__ __forceinline__ void count_tiles(const GemmArgs& a, int* first) {
   __syncthreads();
 }
 
-// y[i] = v, rounded to y's type.
-__device__ __forceinline__ void store_y(const GemmArgs& a, size_t i, float v) {
-  if (a.y_dtype == HQ_BF16) static_cast<__nv_bfloat16*>(a.y)[i] = __float2bfloat16_rn(v);
-  else if (a.y_dtype == HQ_F16) static_cast<__half*>(a.y)[i] = __float2half_rn(v);
-  else static_cast<float*>(a.y)[i] = v;
+// Rows y[0 .. n) of one column from P columns of a lane's accumulator.
+template <int P, typename T>
+__device__ __forceinline__ void store_column(T* y, size_t ldy, const float (&f)[P], int n) {
+  if (n >= P) {
+#pragma unroll
+    for (int j = 0; j < P; ++j, y += ldy) *y = from_f32<T>(f[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < P; ++j, y += ldy) {
+      if (j < n) *y = from_f32<T>(f[j]);
+    }
+  }
+}
+
+template <int P>
+__device__ __forceinline__ void store_any(const GemmArgs& a, size_t row, int m, const float (&f)[P], int n) {
+  const size_t o = row * a.ldy + m;
+  if (a.y_dtype == HQ_BF16) store_column<P>(static_cast<__nv_bfloat16*>(a.y) + o, a.ldy, f, n);
+  else if (a.y_dtype == HQ_F16) store_column<P>(static_cast<__half*>(a.y) + o, a.ldy, f, n);
+  else store_column<P>(static_cast<float*>(a.y) + o, a.ldy, f, n);
+}
+
+// P (16 or 32) accumulator columns from c on.
+template <int P>
+__device__ __forceinline__ void load_columns(uint32_t d, float (&f)[P]) {
+  uint32_t v[P / 16][16];
+#pragma unroll
+  for (int i = 0; i < P / 16; ++i) tc::tc_ld16(d + 16 * i, v[i]);
+  tc::tc_wait_ld();
+#pragma unroll
+  for (int i = 0; i < P / 16; ++i) {
+    tc::tc_tie16(v[i]);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) f[16 * i + j] = __uint_as_float(v[i][j]);
+  }
 }
 
 // ------------------------------------------------------------------ kernel
@@ -280,7 +333,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   uint64_t* epi = dempty + S::kAccs;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(epi + 1);
   uint32_t* flag = tslot + 1;
-  __shared__ int first[GROUPED ? kMaxGroups + 1 : 1];
+  __shared__ int first[GROUPED ? 3 * kMaxGroups + 1 : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -309,7 +362,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   const uint32_t sf_cols = tmem + S::kAccs * S::kW * NT;
   if constexpr (GROUPED) {
     pdl_wait();  // the segments come from the sort
-    count_tiles<NT>(a, first);
+    load_groups<NT>(a, first);
   }
   bool ok = true;
 
@@ -546,18 +599,14 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(dempty + acc);
       } else if (whole) {
-        for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
-          uint32_t v[16];
-          tc::tc_ld16(d + c, v);
-          tc::tc_wait_ld();
-          tc::tc_tie16(v);
+        constexpr int P = NT / kParts < 32 ? 16 : 32;
+        for (int c = col0; c < col1 && c < it.n_valid; c += P) {
+          float f[P];
+          load_columns<P>(d + c, f);
           if (m < a.M) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (c + i < it.n_valid) {
-                store_y(a, static_cast<size_t>(it.n0 + c + i) * a.ldy + m, __uint_as_float(v[i]) * alpha);
-              }
-            }
+            for (int j = 0; j < P; ++j) f[j] *= alpha;
+            store_any<P>(a, it.n0 + c, m, f, it.n_valid - c);
           }
         }
         tc::tc_fence_before();
@@ -573,12 +622,10 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         // a CTA's second slot is for the tile that it begins
         float* mine = a.part + (2 * static_cast<size_t>(blockIdx.x) + (it.c0 == 0 ? 1 : 0)) * part_size;
         for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
-          uint32_t v[16];
-          tc::tc_ld16(d + c, v);
-          tc::tc_wait_ld();
-          tc::tc_tie16(v);
+          float f[16];
+          load_columns<16>(d + c, f);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) __stcg(mine + (c + i) * kM + mrow, __uint_as_float(v[i]));
+          for (int i = 0; i < 16; ++i) __stcg(mine + (c + i) * kM + mrow, f[i]);
         }
         tc::tc_fence_before();
         __threadfence();
@@ -612,9 +659,8 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
             }
             if (m < a.M) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if (c + j < it.n_valid) store_y(a, static_cast<size_t>(it.n0 + c + j) * a.ldy + m, f[j] * alpha);
-              }
+              for (int j = 0; j < 16; ++j) f[j] *= alpha;
+              store_any<16>(a, it.n0 + c, m, f, it.n_valid - c);
             }
           }
           if (ew == 0 && lane == 0) a.counters[i0] = 0;

@@ -48,7 +48,8 @@ struct QuantArgs {
   int rows_pad;   // rows whose scales are written (whole tiles; beyond `rows`: zero)
   int K;
   int c_pad;      // 16-value chunks per row of whole scale tiles
-  int lanes_log;  // log2 of the threads along a row
+  int cpb, rpb;   // chunks and rows of one block (a piece of one row, or whole rows)
+  uint32_t inv;   // 65536 / cpb rounded up: tid / cpb for a block's threads
   const float* ts;
   uint8_t* codes;
   uint8_t* scales;
@@ -64,10 +65,14 @@ template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lanes = 1 << a.lanes_log;
-  const long row = static_cast<long>(blockIdx.x) * (kThreads >> a.lanes_log) + (threadIdx.x >> a.lanes_log);
-  const int c = blockIdx.y * lanes + (threadIdx.x & (lanes - 1));
-  const bool live = row < a.rows && c * 16 < a.K;
+  // Rows from the last to the first: what wrote x, or read it for its largest
+  // value, did the end last, and that part may still lie in L2.
+  const int r = static_cast<int>(threadIdx.x * a.inv >> 16);
+  const int cb = threadIdx.x - r * a.cpb;
+  const long row = static_cast<long>(gridDim.x - 1 - blockIdx.x) * a.rpb + r;
+  const int c = blockIdx.y * a.cpb + cb;
+  const bool mine = r < a.rpb && c < a.c_pad;
+  const bool live = mine && row < a.rows && c * 16 < a.K;
   float v[16];
   if (live) {
     load_chunk<T, 16>(static_cast<const T*>(a.x) + row * a.ldx + c * 16, v);
@@ -83,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
   uint32_t sw = byte << (8 * (c >> S & 3));
   sw |= __shfl_xor_sync(~0u, sw, 1 << S);
   sw |= __shfl_xor_sync(~0u, sw, 2 << S);
-  const bool scale_lane = (c & ((4 << S) - 1)) == 0 && c < a.c_pad;
+  const bool scale_lane = mine && (c & ((4 << S) - 1)) == 0;
   const int st = c >> (2 + S);  // scale tile along K
   if (a.pos == nullptr) {
     if (live) *reinterpret_cast<uint2*>(a.codes + row * (a.K / 2) + c * 8) = p.codes;
@@ -99,10 +104,10 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
     }
   } else if (row < a.rows) {
     for (int j = 0; j < a.k; ++j) {
-      const int r = __ldg(a.pos + row * a.k + j);
-      if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.dst_rows)) continue;
-      if (live) *reinterpret_cast<uint2*>(a.codes + static_cast<long>(r) * (a.K / 2) + c * 8) = p.codes;
-      if (scale_lane) *reinterpret_cast<uint32_t*>(a.scales + scale_cell(r, st, a.kb)) = sw;
+      const int dst = __ldg(a.pos + row * a.k + j);
+      if (static_cast<uint32_t>(dst) >= static_cast<uint32_t>(a.dst_rows)) continue;
+      if (live) *reinterpret_cast<uint2*>(a.codes + static_cast<long>(dst) * (a.K / 2) + c * 8) = p.codes;
+      if (scale_lane) *reinterpret_cast<uint32_t*>(a.scales + scale_cell(dst, st, a.kb)) = sw;
     }
   }
 }
@@ -148,9 +153,9 @@ __global__ void __launch_bounds__(kThreads) tensor_scale_kernel(const T* __restr
 
 template <typename T>
 cudaError_t quantize_launch(int fmt, const QuantArgs& a, dim3 grid, cudaStream_t st) {
-  return fmt == HQ_FP4_NV
-             ? launch_pdl(quantize_rows_kernel<T, HQ_FP4_NV>, grid, dim3(kThreads), 0, st, true, a)
-             : launch_pdl(quantize_rows_kernel<T, HQ_FP4_MX>, grid, dim3(kThreads), 0, st, true, a);
+  const dim3 block((a.cpb * a.rpb + 31) / 32 * 32);
+  return fmt == HQ_FP4_NV ? launch_pdl(quantize_rows_kernel<T, HQ_FP4_NV>, grid, block, 0, st, true, a)
+                          : launch_pdl(quantize_rows_kernel<T, HQ_FP4_MX>, grid, block, 0, st, true, a);
 }
 
 }  // namespace
@@ -166,8 +171,10 @@ cudaError_t launch_quantize(int fmt, hq_dtype xd, const void* x, size_t ldx, int
   a.K = K;
   a.kb = scale_tiles(fmt, K);
   a.c_pad = a.kb * (fmt == HQ_FP4_NV ? 4 : 8);
-  a.lanes_log = 3;  // whole scale words within a warp
-  while ((1 << a.lanes_log) < a.c_pad && a.lanes_log < 8) ++a.lanes_log;
+  const int pieces = (a.c_pad + kThreads - 1) / kThreads;
+  a.cpb = ((a.c_pad + pieces - 1) / pieces + 7) / 8 * 8;  // whole scale words
+  a.rpb = pieces > 1 ? 1 : std::max(1, kThreads / a.cpb);
+  a.inv = (65536 + a.cpb - 1) / a.cpb;
   a.ts = ts;
   a.codes = codes;
   a.scales = scales;
@@ -175,8 +182,7 @@ cudaError_t launch_quantize(int fmt, hq_dtype xd, const void* x, size_t ldx, int
   a.pos = pos;
   a.k = k;
   a.dst_rows = dst_rows;
-  const int per = kThreads >> a.lanes_log;
-  const dim3 grid((a.rows_pad + per - 1) / per, (a.c_pad + (1 << a.lanes_log) - 1) >> a.lanes_log);
+  const dim3 grid((a.rows_pad + a.rpb - 1) / a.rpb, pieces);
   switch (xd) {
     case HQ_F16: return quantize_launch<__half>(fmt, a, grid, st);
     case HQ_BF16: return quantize_launch<__nv_bfloat16>(fmt, a, grid, st);
