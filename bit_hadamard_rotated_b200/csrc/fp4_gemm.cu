@@ -58,6 +58,23 @@ constexpr int kSmemMax = 218 * 1024;  // dynamic; the experts' segments (12 KB) 
 
 // ------------------------------------------------------------------ PTX
 
+// One lane of a converged warp (the same one every time).  The warps that issue
+// copies and MMAs run their loops with all lanes on warp-uniform values and
+// elect a lane around the instructions only: their operands are then computed
+// in uniform registers, which these instructions take.  From one lane in a
+// divergent branch every operand is moved over first, and an MMA took about 115
+// cycles to issue, a chunk of four with its waits about 900.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(~0u, v, 0); }
+// A wait that all lanes of a warp agree on.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(~0u, mbar_wait(bar, parity));
+}
+
 // 8 consecutive 32-bit tensor-memory columns of this thread's lane.
 __device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
@@ -179,22 +196,23 @@ struct Walk {
   __device__ __forceinline__ Walk(const GemmArgs& a, const int* groups) : first(groups) {
     if constexpr (GROUPED) {
       // an even run of tiles per CTA, m tiles fastest
-      const long all = first[a.E];
+      const long all = uniform(first[a.E]);
       u = static_cast<int>(all * blockIdx.x / gridDim.x);
       end = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
       e = 0;
       int n = a.E;  // the expert whose tiles include u: first[e] <= u < first[e + 1]
       while (n > 1) {
         const int h = n >> 1;
-        if (first[e + h] <= u) {
+        if (uniform(first[e + h]) <= u) {
           e += h;
           n -= h;
         } else {
           n = h;
         }
       }
-      ni = (u - first[e]) / a.mt;
-      mi = u - first[e] - ni * a.mt;
+      const int t = u - uniform(first[e]);
+      ni = t / a.mt;
+      mi = t - ni * a.mt;
     } else if (a.units == 0) {
       u = blockIdx.x;
       end = a.mt * a.nt;
@@ -214,13 +232,14 @@ struct Walk {
         mi = 0;
         ++ni;
       }
-      while (ni * NT >= starts[a.E + e]) {  // the next expert that has rows
-        ++e;
+      int rows = uniform(starts[a.E + e]);
+      while (ni * NT >= rows) {  // the next expert that has rows
+        rows = uniform(starts[a.E + ++e]);
         ni = 0;
       }
       it.m0 = mi * kM;
-      it.n0 = starts[e] + ni * NT;
-      it.n_valid = min(NT, starts[a.E + e] - ni * NT);
+      it.n0 = uniform(starts[e]) + ni * NT;
+      it.n_valid = min(NT, rows - ni * NT);
       it.w_row = e * a.M + it.m0;
       it.e = e;
       ++mi;
@@ -334,7 +353,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(epi + 1);
   uint32_t* flag = tslot + 1;
   __shared__ int first[GROUPED ? 3 * kMaxGroups + 1 : 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(full + i, 1);
@@ -367,127 +386,132 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   bool ok = true;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const bool early = !GROUPED && a.early != 0;
-      if (!GROUPED && !early) pdl_wait();
-      Walk<NT, GROUPED> w(a, first);
-      Item it;
-      int slot = 0, turn = 0;
-      // With early weights: the first ring of weight copies goes out before the
-      // wait, the token copies of the same slots after it.
-      Walk<NT, GROUPED> w2 = w;
-      Item it2;
-      int ahead = 0;
-      auto bytes_of = [&](const Item& t, int c, int& tiles, int& row_tiles, int& a_rows) {
-        tiles = min(S::kTiles, a.wkb - c * S::kTiles);
-        row_tiles = min(S::kRowTiles, a.a_row_tiles - (t.n0 >> 7));
-        a_rows = GROUPED ? (t.n_valid + 15) / 16 * 16 : NT;
-        return static_cast<uint32_t>(S::kW * kWBytes + a_rows * 128 + tiles * 512 * (S::kW + row_tiles));
-      };
-      auto weights = [&](const Item& t, int c, int s) {
-        int tiles, row_tiles, a_rows;
-        const uint32_t bytes = bytes_of(t, c, tiles, row_tiles, a_rows);
-        uint8_t* p = ring + s * S::kSlot;
-        mbar_arrive_expect_tx(full + s, bytes);
+    const bool early = !GROUPED && a.early != 0;
+    if (!GROUPED && !early) pdl_wait();
+    Walk<NT, GROUPED> w(a, first);
+    Item it;
+    int slot = 0, turn = 0;
+    struct Sizes {
+      int tiles, row_tiles, a_rows;
+      uint32_t bytes;
+    };
+    auto sizes = [&](const Item& t, int c) {
+      Sizes z;
+      z.tiles = min(S::kTiles, a.wkb - c * S::kTiles);
+      z.row_tiles = min(S::kRowTiles, a.a_row_tiles - (t.n0 >> 7));
+      z.a_rows = GROUPED ? (t.n_valid + 15) / 16 * 16 : NT;
+      z.bytes = static_cast<uint32_t>(S::kW * kWBytes + z.a_rows * 128 + z.tiles * 512 * (S::kW + z.row_tiles));
+      return z;
+    };
+    auto weights = [&](const Item& t, int c, int s, const Sizes& z) {
+      uint8_t* p = ring + s * S::kSlot;
+      const size_t sf = (static_cast<size_t>(t.w_row >> 7) * a.wkb + c * S::kTiles) * 512;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full + s, z.bytes);
         tma_load_2d(p, &wmap, c * (kChunk / 2), t.w_row, full + s);
-        const size_t sf = (static_cast<size_t>(t.w_row >> 7) * a.wkb + c * S::kTiles) * 512;
-        bulk_g2s(p + S::kSfOff, a.wsf + sf, tiles * 512, full + s);
+        bulk_g2s(p + S::kSfOff, a.wsf + sf, z.tiles * 512, full + s);
         if constexpr (MODE == kGated) {
           tma_load_2d(p + kWBytes, &wmap2, c * (kChunk / 2), t.w_row, full + s);
-          bulk_g2s(p + S::kSfOff + S::kSf, a.wsf2 + sf, tiles * 512, full + s);
+          bulk_g2s(p + S::kSfOff + S::kSf, a.wsf2 + sf, z.tiles * 512, full + s);
         }
-      };
-      auto tokens = [&](const Item& t, int c, int s) {
-        int tiles, row_tiles, a_rows;
-        bytes_of(t, c, tiles, row_tiles, a_rows);
-        uint8_t* p = ring + s * S::kSlot;
+      }
+    };
+    auto tokens = [&](const Item& t, int c, int s, const Sizes& z) {
+      uint8_t* p = ring + s * S::kSlot;
+      const uint8_t* sf = a.asf + (static_cast<size_t>(t.n0 >> 7) * a.wkb + c * S::kTiles) * 512;
+      const size_t next = static_cast<size_t>(a.wkb) * 512;
+      if (elect_one()) {
         if constexpr (GROUPED) {
-          for (int r = 0; r < a_rows; r += 16) {
+          for (int r = 0; r < z.a_rows; r += 16) {
             tma_load_2d(p + S::kW * kWBytes + r * 128, &amap, c * (kChunk / 2), t.n0 + r, full + s);
           }
         } else {
           tma_load_2d(p + S::kW * kWBytes, &amap, c * (kChunk / 2), t.n0, full + s);
         }
-        for (int r = 0; r < row_tiles; ++r) {
-          bulk_g2s(p + S::kSfOff + (S::kW + r) * S::kSf,
-                   a.asf + (static_cast<size_t>((t.n0 >> 7) + r) * a.wkb + c * S::kTiles) * 512, tiles * 512,
-                   full + s);
-        }
-      };
-      if (early) {
-        bool more = true;
-        while (more && ahead < ST) {
-          more = w2.next(a, it2);
-          if (!more) break;
-          for (int c = it2.c0; c < it2.c1 && ahead < ST; ++c) weights(it2, c, ahead++);
-        }
-        pdl_wait();
-      }
-      int n = 0;  // chunks so far
-      while (ok && w.next(a, it)) {
-        for (int c = it.c0; c < it.c1; ++c) {
-          if (n >= ST && !mbar_wait(empty + slot, turn ^ 1)) {
-            ok = false;
-            break;
-          }
-          if (n >= ahead) weights(it, c, slot);
-          tokens(it, c, slot);
-          ++n;
-          if (++slot == ST) {
-            slot = 0;
-            turn ^= 1;
-          }
+        bulk_g2s(p + S::kSfOff + S::kW * S::kSf, sf, z.tiles * 512, full + s);
+        if (S::kRowTiles > 1 && z.row_tiles > 1) {
+          bulk_g2s(p + S::kSfOff + (S::kW + 1) * S::kSf, sf + next, z.tiles * 512, full + s);
         }
       }
-      pdl_launch_dependents();
+    };
+    static_assert(S::kRowTiles <= 2, "token scale tiles");
+    // With early weights the first ring of weight copies goes out before the
+    // wait for the preceding kernel, the token copies of those slots after it.
+    int ahead = 0;
+    if (early) {
+      Walk<NT, GROUPED> w2 = w;
+      while (ahead < ST && w2.next(a, it)) {
+        for (int c = it.c0; c < it.c1 && ahead < ST; ++c, ++ahead) weights(it, c, ahead, sizes(it, c));
+      }
+      pdl_wait();
     }
+    int n = 0;  // chunks so far
+    while (ok && w.next(a, it)) {
+      for (int c = it.c0; c < it.c1; ++c) {
+        if (n >= ST && !warp_wait(empty + slot, turn ^ 1)) {
+          ok = false;
+          break;
+        }
+        const Sizes z = sizes(it, c);
+        if (n >= ahead) weights(it, c, slot, z);
+        tokens(it, c, slot, z);
+        ++n;
+        if (++slot == ST) {
+          slot = 0;
+          turn ^= 1;
+        }
+      }
+    }
+    pdl_launch_dependents();
   } else if (warp == 1) {
-    if (lane == 0) {
-      Walk<NT, GROUPED> w(a, first);
-      Item it;
-      int slot = 0, par = 0, acc = 0, accn = 0;
-      while (ok && w.next(a, it)) {
-        const uint32_t d = tmem + acc * S::kW * NT;
-        if (accn >= S::kAccs && !mbar_wait(dempty + acc, (accn / S::kAccs - 1) & 1)) {
+    const uint32_t d0 = uniform(tmem), sf0 = uniform(sf_cols), ring0 = uniform(smem_u32(ring));
+    Walk<NT, GROUPED> w(a, first);
+    Item it;
+    int slot = 0, par = 0, acc = 0, accn = 0;
+    while (ok && w.next(a, it)) {
+      const uint32_t d = d0 + acc * S::kW * NT;
+      if (accn >= S::kAccs && !warp_wait(dempty + acc, (accn / S::kAccs - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      const int n_mma = (it.n_valid + 15) / 16 * 16;
+      // the tokens' rows within their scale tile: 0 or 64 (two columns)
+      const uint32_t half = NT < 128 ? ((it.n0 & 127) >> 5) : 0;
+      for (int c = it.c0; c < it.c1; ++c) {
+        if (!warp_wait(full + slot, par) || !warp_wait(sfull + slot, par)) {
           ok = false;
           break;
         }
         tc::tc_fence_after();
-        const int n_mma = (it.n_valid + 15) / 16 * 16;
-        for (int c = it.c0; c < it.c1; ++c) {
-          if (!mbar_wait(full + slot, par) || !mbar_wait(sfull + slot, par)) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const uint32_t p = smem_u32(ring + slot * S::kSlot);
-          const uint32_t sfa = sf_cols + slot * S::kSfCols, sfb = sfa + S::kW * S::kTiles * 4;
-          const uint64_t db = desc_sw128(p + S::kW * kWBytes);
-          // the tokens' rows within their scale tile: 0 or 64 (two columns)
-          const uint32_t half = NT < 128 ? ((it.n0 & 127) >> 5) : 0;
-          const int steps = min(4, a.k_steps - 4 * c);
+        const uint32_t p = ring0 + slot * S::kSlot;
+        const uint32_t sfa = sf0 + slot * S::kSfCols, sfb = sfa + S::kW * S::kTiles * 4 + half;
+        const uint64_t da = desc_sw128(p), db = desc_sw128(p + S::kW * kWBytes);
+        const int steps = min(4, a.k_steps - 4 * c);
+        const uint32_t first_sum = c > it.c0 ? 1u : 0u;
+        if (elect_one()) {
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            if (s >= steps) break;
+            if (s < steps) {
 #pragma unroll
-            for (int i = 0; i < S::kW; ++i) {
-              const int t = FMT == HQ_FP4_NV ? s : s >> 1, id = FMT == HQ_FP4_NV ? 0 : 2 * (s & 1);
-              tc_mma_scaled<FMT>(d + i * NT, desc_sw128(p + i * kWBytes) + 2 * s, db + 2 * s, idesc_fp4(FMT, n_mma, id),
-                                 sfa + 4 * (i * S::kTiles + t), sfb + 4 * t * S::kRowTiles + half,
-                                 (c > it.c0 || s > 0) ? 1u : 0u);
+              for (int i = 0; i < S::kW; ++i) {
+                const int t = FMT == HQ_FP4_NV ? s : s >> 1, id = FMT == HQ_FP4_NV ? 0 : 2 * (s & 1);
+                tc_mma_scaled<FMT>(d + i * NT, da + i * (kWBytes >> 4) + 2 * s, db + 2 * s, idesc_fp4(FMT, n_mma, id),
+                                   sfa + 4 * (i * S::kTiles + t), sfb + 4 * t * S::kRowTiles,
+                                   s > 0 ? 1u : first_sum);
+              }
             }
           }
           tc::tc_commit(empty + slot);
-          if (++slot == ST) {
-            slot = 0;
-            par ^= 1;
-          }
+          if (c + 1 == it.c1) tc::tc_commit(dfull + acc);
         }
-        if (!ok) break;
-        tc::tc_commit(dfull + acc);
-        ++accn;
-        acc = accn % S::kAccs;
+        if (++slot == ST) {
+          slot = 0;
+          par ^= 1;
+        }
       }
+      ++accn;
+      acc = accn % S::kAccs;
     }
   } else if (warp < 6) {
     const int quarter = warp & 3;
@@ -496,7 +520,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     int slot = 0, par = 0;
     while (ok && w.next(a, it)) {
       for (int c = it.c0; c < it.c1; ++c) {
-        if (!__all_sync(~0u, mbar_wait(full + slot, par))) {
+        if (!warp_wait(full + slot, par)) {
           ok = false;
           break;
         }
@@ -538,12 +562,12 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     auto meet = [&]() {  // all epilogue warps, bounded
       __syncwarp();
       if (lane == 0) mbar_arrive(epi);
-      const bool r = __all_sync(~0u, mbar_wait(epi, epar));
+      const bool r = warp_wait(epi, epar);
       epar ^= 1;
       return r;
     };
     while (ok && w.next(a, it)) {
-      if (!__all_sync(~0u, mbar_wait(dfull + acc, (accn / S::kAccs) & 1))) {
+      if (!warp_wait(dfull + acc, (accn / S::kAccs) & 1)) {
         ok = false;
         break;
       }
