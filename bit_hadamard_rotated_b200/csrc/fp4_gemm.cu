@@ -13,17 +13,15 @@
 // One CTA walks a list of (tile, K range) items.  Per 256 values of K it needs
 // 16 KB of weight codes (one TMA box, 128-byte swizzle), the tokens' codes,
 // and the scale tiles (bulk copies), all on one mbarrier per ring slot.
-//   warp 0     producer: one thread issues the copies
-//   warp 1     one thread issues the MMAs (K = 64 each); their commit frees
-//              the slot
-//   warps 2-5  the slot's scales from shared to tensor memory, one column set
-//              per slot (a scale tile is 16 bytes per lane: one vector load and
-//              a share of a 16-column store)
-//   others     epilogue: tensor memory to registers, alpha, one rounding, y
-// The scales go through registers because tcgen05.cp costs its issuing thread
-// about 55 cycles a tile beside about 115 per MMA (128 at N = 256, the pipe's
-// rate): 12 tiles and 4 MMAs of a 256-token chunk took 1164 cycles from one
-// thread, the MMAs alone 512.
+//   warp 0   producer: issues the copies
+//   warp 1   moves the slot's scales to tensor memory (tcgen05.cp) and issues
+//            the MMAs (K = 64 each) behind them, in order; their commit frees
+//            the slot
+//   others   epilogue: tensor memory to registers, alpha, one rounding, y
+// The copies of the scales cost nothing beside the MMAs: 12 of them and 4 MMAs
+// of 256 tokens took 512 cycles, the MMAs' own time (through registers, by
+// four more warps, they took shared-memory bandwidth from the operands: 8192 x
+// 8192 at 4096 tokens 136 us instead of 121).
 // Two accumulators where they fit (up to 128 tokens), so the next tile's MMAs
 // run under the epilogue.
 //
@@ -75,11 +73,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(~0u, mbar_wait(bar, parity));
 }
 
-// 8 consecutive 32-bit tensor-memory columns of this thread's lane.
-__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+// Scale tile (512 bytes) to four tensor-memory columns, in all four lane
+// quarters.
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t smem) {
+  const uint64_t desc = tc::smem_desc(smem, 0, 128);
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // D (+)= (A sA) (B sB), K = 64, E2M1, A and B K-major in shared memory.
@@ -136,15 +134,14 @@ struct Shape {
   static constexpr int kAccs = kW * NT <= 128 ? 2 : 1;                   // accumulator sets
   static constexpr int kSfCols = kTiles * 4 * (kW + kRowTiles);          // one slot's scales
   static constexpr int kEpiWarps = 8;
-  static constexpr int kThreads = 64 + 128 + 32 * kEpiWarps;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kTurn = MODE == kGated ? kEpiWarps * 16 * kTurnRow * 4 : 0;  // epilogue transposes
   static constexpr int kFit = (kSmemMax - kTurn - 2048 - (MODE == kDense ? 0 : 4096)) / kSlot;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
-  static constexpr int kColsNeeded = kAccs * kW * NT + kStages * kSfCols;
+  static constexpr int kColsNeeded = kAccs * kW * NT + 2 * kSfCols;
   static constexpr int kCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kSlot + kTurn + 512;
   static_assert(kColsNeeded <= 512, "tensor memory");
-  static_assert(kSfCols % 8 == 0, "whole stores");
   static_assert(kSlot % 1024 == 0, "swizzle atoms");
 };
 
@@ -346,8 +343,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   float* turn_buf = reinterpret_cast<float*>(ring + ST * S::kSlot);
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + ST * S::kSlot + S::kTurn);
   uint64_t* empty = full + ST;
-  uint64_t* sfull = empty + ST;
-  uint64_t* dfull = sfull + ST;
+  uint64_t* dfull = empty + ST;
   uint64_t* dempty = dfull + S::kAccs;
   uint64_t* epi = dempty + S::kAccs;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(epi + 1);
@@ -358,7 +354,6 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     for (int i = 0; i < ST; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
-      mbar_init(sfull + i, 4);
     }
     for (int i = 0; i < S::kAccs; ++i) {
       mbar_init(dfull + i, 1);
@@ -467,7 +462,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     const uint32_t d0 = uniform(tmem), sf0 = uniform(sf_cols), ring0 = uniform(smem_u32(ring));
     Walk<NT, GROUPED> w(a, first);
     Item it;
-    int slot = 0, par = 0, acc = 0, accn = 0;
+    int slot = 0, par = 0, acc = 0, accn = 0, n = 0;
     while (ok && w.next(a, it)) {
       const uint32_t d = d0 + acc * S::kW * NT;
       if (accn >= S::kAccs && !warp_wait(dempty + acc, (accn / S::kAccs - 1) & 1)) {
@@ -479,17 +474,27 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       // the tokens' rows within their scale tile: 0 or 64 (two columns)
       const uint32_t half = NT < 128 ? ((it.n0 & 127) >> 5) : 0;
       for (int c = it.c0; c < it.c1; ++c) {
-        if (!warp_wait(full + slot, par) || !warp_wait(sfull + slot, par)) {
+        if (!warp_wait(full + slot, par)) {
           ok = false;
           break;
         }
         tc::tc_fence_after();
         const uint32_t p = ring0 + slot * S::kSlot;
-        const uint32_t sfa = sf0 + slot * S::kSfCols, sfb = sfa + S::kW * S::kTiles * 4 + half;
+        const uint32_t sfa = sf0 + (n & 1) * S::kSfCols, sfb = sfa + S::kW * S::kTiles * 4, sp = p + S::kSfOff;
         const uint64_t da = desc_sw128(p), db = desc_sw128(p + S::kW * kWBytes);
         const int steps = min(4, a.k_steps - 4 * c);
         const uint32_t first_sum = c > it.c0 ? 1u : 0u;
+        ++n;
         if (elect_one()) {
+#pragma unroll
+          for (int t = 0; t < S::kTiles; ++t) {
+#pragma unroll
+            for (int i = 0; i < S::kW; ++i) tc_copy_scales(sfa + 4 * (i * S::kTiles + t), sp + i * S::kSf + 512 * t);
+#pragma unroll
+            for (int r = 0; r < S::kRowTiles; ++r) {
+              tc_copy_scales(sfb + 4 * (t * S::kRowTiles + r), sp + S::kSf * (S::kW + r) + 512 * t);
+            }
+          }
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             if (s < steps) {
@@ -497,7 +502,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
               for (int i = 0; i < S::kW; ++i) {
                 const int t = FMT == HQ_FP4_NV ? s : s >> 1, id = FMT == HQ_FP4_NV ? 0 : 2 * (s & 1);
                 tc_mma_scaled<FMT>(d + i * NT, da + i * (kWBytes >> 4) + 2 * s, db + 2 * s, idesc_fp4(FMT, n_mma, id),
-                                   sfa + 4 * (i * S::kTiles + t), sfb + 4 * t * S::kRowTiles,
+                                   sfa + 4 * (i * S::kTiles + t), sfb + 4 * t * S::kRowTiles + half,
                                    s > 0 ? 1u : first_sum);
               }
             }
@@ -513,45 +518,9 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       ++accn;
       acc = accn % S::kAccs;
     }
-  } else if (warp < 6) {
-    const int quarter = warp & 3;
-    Walk<NT, GROUPED> w(a, first);
-    Item it;
-    int slot = 0, par = 0;
-    while (ok && w.next(a, it)) {
-      for (int c = it.c0; c < it.c1; ++c) {
-        if (!warp_wait(full + slot, par)) {
-          ok = false;
-          break;
-        }
-        const uint32_t sp = smem_u32(ring + slot * S::kSlot + S::kSfOff) + lane * 16;
-        uint32_t v[S::kSfCols];
-#pragma unroll
-        for (int i = 0; i < S::kSfCols / 4; ++i) {
-          // columns: the weights' tiles, then the tokens', row tiles innermost
-          constexpr int kWTiles = S::kW * S::kTiles;
-          const int j = i - kWTiles;
-          const int at = i < kWTiles ? i * 512 : (S::kW + j % S::kRowTiles) * S::kSf + j / S::kRowTiles * 512;
-          const uint4 u = lds128(sp + at);
-          v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
-        }
-        const uint32_t dst = sf_cols + slot * S::kSfCols + (static_cast<uint32_t>(quarter * 32) << 16);
-#pragma unroll
-        for (int i = 0; i < S::kSfCols; i += 8) tc_st8(dst + i, v + i);
-        tc::tc_wait_st();
-        tc::tc_fence_before();
-        fence_proxy_async_smem();  // the reads above come before the slot's next copies
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sfull + slot);
-        if (++slot == ST) {
-          slot = 0;
-          par ^= 1;
-        }
-      }
-    }
   } else {
     if constexpr (!GROUPED) pdl_wait();
-    const int ew = warp - 6, quarter = warp & 3;
+    const int ew = warp - 2, quarter = warp & 3;
     constexpr int kParts = S::kEpiWarps / 4;  // warps that share a lane quarter split the columns
     const int col0 = (ew >> 2) * (NT / kParts), col1 = col0 + NT / kParts;
     const int mrow = quarter * 32 + lane;

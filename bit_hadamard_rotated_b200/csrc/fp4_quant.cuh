@@ -28,18 +28,46 @@ __device__ __forceinline__ void block_scale(float amax, float ts, uint32_t& byte
   }
 }
 
-// x / eff for 16 values.  Where 1 / eff is far from under- and overflow, by
-// Markstein's quotient correction (IBM J. Res. Dev. 34, 1990): with y the
-// correctly rounded 1 / eff, q = x y is within an ulp and q + (x - q eff) y,
-// both steps fused, rounds to the correctly rounded quotient; so ties between
-// codes are met exactly, at 3 operations a value instead of a division.
+// Two fp32 values in one 64-bit register pair, for the packed fp32 pipe.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void un2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// x / eff for 16 values.  An E8M0 scale is a power of two and so is its
+// reciprocal (2^-125 to 2^127): one exact product.  Otherwise, where 1 / eff is
+// far from under- and overflow, by Markstein's quotient correction (IBM J. Res.
+// Dev. 34, 1990): with y the correctly rounded 1 / eff, q = x y is within an
+// ulp and q + (x - q eff) y, both steps fused, rounds to the correctly rounded
+// quotient; so ties between codes are met exactly, at 3 packed operations for
+// two values instead of two divisions.
+template <int FMT>
 __device__ __forceinline__ void quotients(float (&v)[16], float eff) {
-  if (eff >= 0x1p-100f && eff <= 0x1p100f) {
-    const float y = __frcp_rn(eff);
+  if (FMT == HQ_FP4_MX || (eff >= 0x1p-100f && eff <= 0x1p100f)) {
+    const float yf = FMT == HQ_FP4_MX ? __uint_as_float(static_cast<uint32_t>(
+                                            254 - max(static_cast<int>(__float_as_uint(eff) >> 23), 0)) << 23)
+                                      : __frcp_rn(eff);
+    const uint64_t y = f2(yf, yf), n = f2(-eff, -eff);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float q = __fmul_rn(v[i], y);
-      v[i] = __fmaf_rn(__fmaf_rn(-q, eff, v[i]), y, q);
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t x = f2(v[2 * i], v[2 * i + 1]);
+      uint64_t q = mul2(x, y);
+      if constexpr (FMT == HQ_FP4_NV) q = fma2(fma2(q, n, x), y, q);
+      un2(q, v[2 * i], v[2 * i + 1]);
     }
   } else if (eff > 0.f) {
 #pragma unroll
@@ -50,13 +78,18 @@ __device__ __forceinline__ void quotients(float (&v)[16], float eff) {
   }
 }
 
-// Two values to two E2M1 codes (low nibble first), round to nearest even,
+// Eight values to eight E2M1 codes (low nibble first), round to nearest even,
 // saturating.
-__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t to_e2m1x8(const float* v) {
   uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
 
@@ -76,33 +109,23 @@ struct Packed16 {
 // values, lanes `mate` apart (all lanes of the warp take part).
 template <int FMT>
 __device__ __forceinline__ Packed16 pack16(float (&v)[16], float ts, int mate) {
-  float amax = 0.f;
-  bool fine = true;  // every value finite
+  // The largest magnitude as a bit pattern: magnitudes order as their
+  // patterns, infinity and NaN lie above all finite ones.
+  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float m = fabsf(v[i]);
-    amax = fmaxf(amax, m);
-    fine = fine && m < INFINITY;
-  }
-  if constexpr (FMT == HQ_FP4_MX) {
-    amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, mate));
-    fine = __shfl_xor_sync(~0u, static_cast<int>(fine), mate) && fine;
-  }
+  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  if constexpr (FMT == HQ_FP4_MX) top = max(top, __shfl_xor_sync(~0u, top, mate));
   Packed16 p;
-  block_scale<FMT>(amax, ts, p.byte, p.eff);
-  if (!fine) {  // the format's NaN as the scale, over codes of zero
+  block_scale<FMT>(__uint_as_float(top), ts, p.byte, p.eff);
+  if (top >= 0x7F800000u) {  // the format's NaN as the scale, over codes of zero
     p.byte = FMT == HQ_FP4_NV ? 0x7Fu : 0xFFu;
     p.eff = __uint_as_float(0x7FC00000u);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
-  } else {
-    quotients(v, p.eff);
+    p.codes = make_uint2(0, 0);
+    return p;
   }
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = to_e2m1x2(v[2 * i], v[2 * i + 1]);
-  p.codes.x = w[0] | w[1] << 8 | w[2] << 16 | w[3] << 24;
-  p.codes.y = w[4] | w[5] << 8 | w[6] << 16 | w[7] << 24;
+  quotients<FMT>(v, p.eff);
+  p.codes.x = to_e2m1x8(v);
+  p.codes.y = to_e2m1x8(v + 8);
   return p;
 }
 

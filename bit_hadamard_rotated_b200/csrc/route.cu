@@ -22,9 +22,10 @@ namespace route {
 namespace {
 
 constexpr int kSortThreads = 1024;
-constexpr int kTile = 8192;         // pairs per sorting block
+constexpr int kMinTile = 2048;      // pairs per sorting block, at least
+constexpr int kMaxTiles = 64;       // blocks of one sort: each reads all blocks' histograms
 constexpr int kMaxExperts = 16384;
-constexpr int kMaxTiles = 1024;     // blocks of one sort (8M pairs)
+constexpr long kMaxPairs = 1l << 23;
 
 // Warps that count a tile side by side: each has its own histogram in shared
 // memory, at most 128 KiB in all.
@@ -34,24 +35,29 @@ __host__ __device__ constexpr int sort_warps(int E) {
 
 struct SortArgs {
   const int32_t* ids;
-  int P, E, align, tiles;
+  int P, E, align, tiles, tile;  // pairs, ..., blocks and pairs per block
   int32_t* pos;
   int32_t* offsets;  // [E + 1]
   int32_t* counts;   // [E]
   int32_t* hist;     // [tiles][E] (more than one tile)
 };
 
-// The pairs of warp w's share of tile b, 32 at a time.
+// The pairs of warp w's share of tile b, 32 at a time; four loads in flight.
 template <typename F>
 __device__ __forceinline__ void each_pair(const SortArgs& a, int b, int w, int W, F&& f) {
   const int lane = threadIdx.x & 31;
-  const int per = (kTile / W + 31) / 32 * 32;
-  const int t1 = min(a.P, (b + 1) * kTile);
-  const int p1 = min(t1, b * kTile + (w + 1) * per);
-  for (int p = b * kTile + w * per; p < p1; p += 32) {
-    const int i = p + lane;
-    const int id = i < p1 ? __ldg(a.ids + i) : -1;
-    f(i, i < p1, id, static_cast<uint32_t>(id) < static_cast<uint32_t>(a.E));
+  const int t0 = b * a.tile, t1 = min(a.P, t0 + a.tile);
+  const int per = ((t1 - t0 + W - 1) / W + 31) / 32 * 32;
+  const int p1 = min(t1, t0 + (w + 1) * per);
+  for (int p = t0 + w * per; p < p1; p += 128) {
+    int id[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) id[u] = p + 32 * u + lane < p1 ? __ldg(a.ids + p + 32 * u + lane) : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = p + 32 * u + lane;
+      if (p + 32 * u < p1) f(i, i < p1, id[u], static_cast<uint32_t>(id[u]) < static_cast<uint32_t>(a.E));
+    }
   }
 }
 
@@ -79,6 +85,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs
   const int W = sort_warps(a.E);
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
     int n = 0;
+#pragma unroll 8
     for (int w = 0; w < W; ++w) n += h[w * a.E + e];
     a.hist[static_cast<size_t>(blockIdx.x) * a.E + e] = n;
   }
@@ -100,8 +107,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
     int total = 0, before = 0;
     if (e < a.E) {
       if (a.tiles == 1) {
+#pragma unroll 8
         for (int i = 0; i < W; ++i) total += h[i * a.E + e];
       } else {
+#pragma unroll 8
         for (int b = 0; b < a.tiles; ++b) {
           const int n = __ldcg(a.hist + static_cast<size_t>(b) * a.E + e);
           before += b < static_cast<int>(blockIdx.x) ? n : 0;
@@ -137,6 +146,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
         if (e == a.E - 1) a.offsets[a.E] = start + rows;
       }
       int run = start + before;
+#pragma unroll 8
       for (int i = 0; i < W; ++i) {
         const int n = h[i * a.E + e];
         h[i * a.E + e] = run;
@@ -331,21 +341,30 @@ cudaError_t by_type(hq_dtype d, F&& f) {
 
 }  // namespace
 
-size_t sort_workspace_bytes(long pairs, int E) {
-  const long tiles = (pairs + kTile - 1) / kTile;
-  return 256 + (tiles > 1 ? (static_cast<size_t>(tiles) * E * 4 + 255) / 256 * 256 : 0);
+static int sort_tile(long pairs) {
+  const long t = (pairs + kMaxTiles - 1) / kMaxTiles;
+  return static_cast<int>(std::max<long>(kMinTile, (t + kMinTile - 1) / kMinTile * kMinTile));
+}
+static int sort_tiles(long pairs) {
+  const int t = sort_tile(pairs);
+  return static_cast<int>(std::max<long>(1, (pairs + t - 1) / t));
 }
 
-int sort_launches(long pairs) { return pairs > kTile ? 2 : 1; }
+// Room for every smaller number of pairs too.
+size_t sort_workspace_bytes(long pairs, int E) {
+  const long tiles = pairs > kMinTile ? std::min<long>(kMaxTiles, (pairs + kMinTile - 1) / kMinTile) : 0;
+  return 256 + (static_cast<size_t>(tiles) * E * 4 + 255) / 256 * 256;
+}
+
+int sort_launches(long pairs) { return sort_tiles(pairs) > 1 ? 2 : 1; }
 
 bool sort_supported(long pairs, int E, int align) {
-  return E <= kMaxExperts && pairs <= static_cast<long>(kMaxTiles) * kTile &&
-         pairs + static_cast<long>(E) * (align - 1) < 0x7fffffffl;
+  return E <= kMaxExperts && pairs <= kMaxPairs && pairs + static_cast<long>(E) * (align - 1) < 0x7fffffffl;
 }
 
 cudaError_t launch_sort(const int32_t* ids, int pairs, int E, int align, int32_t* pos, int32_t* offsets,
                         int32_t* counts, void* ws, cudaStream_t st) {
-  SortArgs a{ids, pairs, E, align, std::max(1, (pairs + kTile - 1) / kTile), pos, offsets, counts,
+  SortArgs a{ids,     pairs,  E, align, sort_tiles(pairs), sort_tile(pairs), pos, offsets, counts,
              reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 256)};
   const size_t smem = static_cast<size_t>(sort_warps(E)) * E * 4;
   if (a.tiles > 1) {

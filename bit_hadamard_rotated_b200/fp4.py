@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from ._lib import HQ_FP4_MX, HQ_FP4_NV, HqFp4Matrix, check, lib
-from .hq import _DT, _need_cuda, _ptr, _raw_stream
+from .hq import _DT, _need_cuda, _on_device, _ptr, _raw_stream
 
 _FMT = {"nv": HQ_FP4_NV, "mx": HQ_FP4_MX}
 
@@ -83,11 +83,16 @@ def hq_fp4_tensor_scale(x: torch.Tensor, stream=None) -> torch.Tensor:
     largest block at the end of the "nv" format's range (1 for zeros)."""
     _need_cuda(x)
     x = _rows_in(x)
-    with torch.cuda.device(x.device):
-        out = torch.empty((), dtype=torch.float32, device=x.device)
-        ws = torch.zeros(256, dtype=torch.uint8, device=x.device)
-        check(lib().hq_fp4_tensor_scale(_ptr(x), _DT[x.dtype], max(x.stride(0), x.shape[1]), x.shape[0], x.shape[1], _ptr(out),
-                                        _ptr(ws), 256, _raw_stream(stream, x.device.index)), "hq_fp4_tensor_scale")
+    return _on_device(x.device, _tensor_scale, x, stream)
+
+
+def _tensor_scale(x, stream):
+    dev = x.device
+    out = torch.empty((), dtype=torch.float32, device=dev)
+    ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+    check(lib().hq_fp4_tensor_scale(x.data_ptr(), _DT[x.dtype], max(x.stride(0), x.shape[1]), x.shape[0], x.shape[1],
+                                    out.data_ptr(), ws.data_ptr(), 256, _raw_stream(stream, dev.index)),
+          "hq_fp4_tensor_scale")
     return out
 
 
@@ -99,26 +104,30 @@ def hq_fp4_quantize(x: torch.Tensor, fmt: str = "nv", tensor_scale: torch.Tensor
     if fmt not in _FMT:
         raise ValueError('fmt must be "nv" or "mx"')
     x = _rows_in(x)
-    rows, K = x.shape
-    dev = x.device
     if tensor_scale is not None:
         if fmt != "nv":
             raise ValueError('only "nv" takes a tensor scale')
-        _need_scale(tensor_scale, dev)
-    with torch.cuda.device(dev):
-        if values is True:
-            values = torch.empty((rows, K), dtype=x.dtype, device=dev)
-        elif values is False:
-            values = None
-        elif values is not None and (values.dtype != x.dtype or values.shape != x.shape or not values.is_contiguous()
-                                     or values.device != dev):
-            raise ValueError("values must be a contiguous tensor of x's type and shape")
-        q = Fp4Matrix.__new__(Fp4Matrix)._set(
-            torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
-            torch.empty(_scale_shape(fmt, rows, K), dtype=torch.uint8, device=dev), fmt, tensor_scale, values)
-        q.c.K = K  # as given: an odd K is refused below
-        check(lib().hq_fp4_quantize(_ptr(x), _DT[x.dtype], max(x.stride(0), K), q._ref, _ptr(values),
-                                    _raw_stream(stream, dev.index)), "hq_fp4_quantize")
+        _need_scale(tensor_scale, x.device)
+    if values is not True and values is not False and values is not None and (
+            values.dtype != x.dtype or values.shape != x.shape or not values.is_contiguous() or values.device != x.device):
+        raise ValueError("values must be a contiguous tensor of x's type and shape")
+    return _on_device(x.device, _quantize, x, fmt, tensor_scale, values, stream)
+
+
+def _quantize(x, fmt, tensor_scale, values, stream):
+    dev, (rows, K) = x.device, x.shape
+    if values is True:
+        values = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif values is False:
+        values = None
+    q = Fp4Matrix.__new__(Fp4Matrix)._set(
+        torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
+        torch.empty(_scale_shape(fmt, rows, K), dtype=torch.uint8, device=dev), fmt, tensor_scale, values)
+    q.c.K = K  # as given: an odd K is refused below
+    st = lib().hq_fp4_quantize(x.data_ptr(), _DT[x.dtype], max(x.stride(0), K), q._ref,
+                               None if values is None else values.data_ptr(), _raw_stream(stream, dev.index))
+    if st:
+        check(st, "hq_fp4_quantize")
     return q
 
 
@@ -150,11 +159,15 @@ def hq_fp4_matmul(w: Fp4Matrix, a: Fp4Matrix, out_dtype: torch.dtype = torch.flo
     dev = w.codes.device
     if a.codes.device != dev:
         raise ValueError(f"a is on {a.codes.device}, the weights on {dev}")
-    with torch.cuda.device(dev):
-        out, ldy = _out(out, a.rows, w.rows, out_dtype if out is None else out.dtype, dev)
-        ws = _workspace(workspace, int(lib().hq_fp4_matmul_workspace_size(w._ref, a.rows)), dev)
-        check(lib().hq_fp4_matmul(w._ref, a._ref, _ptr(out), _DT[out.dtype], ldy, _ptr(ws), ws.numel(),
-                                  _raw_stream(stream, dev.index)), "hq_fp4_matmul")
+    return _on_device(dev, _matmul, w, a, out_dtype, out, workspace, stream)
+
+
+def _matmul(w, a, out_dtype, out, workspace, stream):
+    dev = w.codes.device
+    out, ldy = _out(out, a.rows, w.rows, out_dtype if out is None else out.dtype, dev)
+    ws = _workspace(workspace, int(lib().hq_fp4_matmul_workspace_size(w._ref, a.rows)), dev)
+    check(lib().hq_fp4_matmul(w._ref, a._ref, out.data_ptr(), _DT[out.dtype], ldy, ws.data_ptr(), ws.numel(),
+                              _raw_stream(stream, dev.index)), "hq_fp4_matmul")
     return out
 
 
@@ -170,13 +183,21 @@ def hq_fp4_linear(w: Fp4Matrix, x: torch.Tensor, x_scale: torch.Tensor | None = 
     if x.device != dev:
         raise ValueError(f"x is on {x.device}, the weights on {dev}")
     _need_scale(x_scale, dev)
-    N = x.shape[0]
-    with torch.cuda.device(dev):
-        out, ldy = _out(out, N, w.rows, (x.dtype if out is None else out.dtype) if out_dtype is None else out_dtype, dev)
-        ws = _workspace(workspace, int(lib().hq_fp4_linear_workspace_size(w._ref, N)), dev)
-        check(lib().hq_fp4_linear(w._ref, _ptr(x), _DT[x.dtype], max(x.stride(0), w.K), N, _ptr(x_scale), _ptr(out),
-                                  _DT[out.dtype], ldy, _ptr(ws), ws.numel(), _raw_stream(stream, dev.index)),
-              "hq_fp4_linear")
+    dtype = out_dtype or (x.dtype if out is None else out.dtype)
+    return _on_device(dev, _linear, w, x, x_scale, dtype, out, workspace, stream)
+
+
+def _linear(w, x, x_scale, dtype, out, workspace, stream):
+    dev, N = w.codes.device, x.shape[0]
+    out, ldy = _out(out, N, w.rows, dtype, dev)
+    ws = workspace
+    if ws is None or ws.device != dev or ws.dtype != torch.uint8:
+        ws = _workspace(ws, int(lib().hq_fp4_linear_workspace_size(w._ref, N)), dev)
+    st = lib().hq_fp4_linear(w._ref, x.data_ptr(), _DT[x.dtype], max(x.stride(0), w.K), N,
+                             None if x_scale is None else x_scale.data_ptr(), out.data_ptr(), _DT[dtype], ldy,
+                             ws.data_ptr(), ws.numel(), _raw_stream(stream, dev.index))
+    if st:
+        check(st, "hq_fp4_linear")
     return out
 
 
@@ -191,22 +212,15 @@ class Fp4Linear:
         self._ws, self._batch = None, 0
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-        w = self.w
-        dev = w.codes.device
-        if not x.is_cuda or x.device != dev:
+        w, dev = self.w, self.w.codes.device
+        if x.device != dev:
             raise ValueError(f"x is on {x.device}, the weights on {dev}")
         x = _rows_in(x, w.K)
         N = x.shape[0]
-        with torch.cuda.device(dev):
-            if N > self._batch or self._ws is None:  # a workspace for N serves every smaller batch
-                self._ws, self._batch = _workspace(None, int(lib().hq_fp4_linear_workspace_size(w._ref, N)), dev), N
-            out, ldy = _out(out, N, w.rows, self.out_dtype or (x.dtype if out is None else out.dtype), dev)
-            st = lib().hq_fp4_linear(w._ref, x.data_ptr(), _DT[x.dtype], max(x.stride(0), w.K), N, _ptr(self.x_scale),
-                                     out.data_ptr(), _DT[out.dtype], ldy, self._ws.data_ptr(), self._ws.numel(),
-                                     _raw_stream(stream, dev.index))
-            if st:
-                check(st, "hq_fp4_linear")
-        return out
+        if N > self._batch or self._ws is None:  # a workspace for N serves every smaller batch
+            self._ws, self._batch = _on_device(dev, _workspace, None, int(lib().hq_fp4_linear_workspace_size(w._ref, N)), dev), N
+        dtype = self.out_dtype or (x.dtype if out is None else out.dtype)
+        return _on_device(dev, _linear, w, x, self.x_scale, dtype, out, self._ws, stream)
 
     def check_status(self, stream=None):
         if self._ws is not None:
@@ -250,23 +264,24 @@ class Fp4Experts:
         for t in (x, topk_ids, topk_w):
             if t.device != dev:
                 raise ValueError(f"a tensor is on {t.device}, the weights on {dev}")
-        k = topk_ids.shape[1]
-        ids, w = topk_ids.contiguous(), topk_w.contiguous()
-        with torch.cuda.device(dev):
-            dtype = self.out_dtype or (x.dtype if out is None else out.dtype)
-            if out is None:
-                out = torch.empty((T, self.hidden), dtype=dtype, device=dev)
-            elif out.dtype != dtype or tuple(out.shape) != (T, self.hidden) or not out.is_contiguous() or out.device != dev:
-                raise ValueError(f"out must be contiguous {dtype} [{T}][{self.hidden}] on {dev}")
-            room = self._room
-            if self._ws is None or T > room[0] or k != room[1] or dtype != room[2]:
-                self._ws, self._room = _workspace(None, self._need(T, k, dtype), dev), (T, k, dtype)
-            st = lib().hq_fp4_experts(self.gate._ref, self.up._ref, self.down._ref, self.n_experts, x.data_ptr(),
-                                      _DT[x.dtype], max(x.stride(0), self.hidden), T, ids.data_ptr(), w.data_ptr(), k,
-                                      _ptr(self.x_scale), _ptr(self.h_scale), out.data_ptr(), _DT[dtype],
-                                      self._ws.data_ptr(), self._ws.numel(), _raw_stream(stream, dev.index))
-            if st:
-                check(st, "hq_fp4_experts")
+        return _on_device(dev, self._call, x, topk_ids.contiguous(), topk_w.contiguous(), out, stream)
+
+    def _call(self, x, ids, w, out, stream):
+        dev, (T, k) = x.device, ids.shape
+        dtype = self.out_dtype or (x.dtype if out is None else out.dtype)
+        if out is None:
+            out = torch.empty((T, self.hidden), dtype=dtype, device=dev)
+        elif out.dtype != dtype or tuple(out.shape) != (T, self.hidden) or not out.is_contiguous() or out.device != dev:
+            raise ValueError(f"out must be contiguous {dtype} [{T}][{self.hidden}] on {dev}")
+        room = self._room
+        if self._ws is None or T > room[0] or k != room[1] or dtype != room[2]:
+            self._ws, self._room = _workspace(None, self._need(T, k, dtype), dev), (T, k, dtype)
+        st = lib().hq_fp4_experts(self.gate._ref, self.up._ref, self.down._ref, self.n_experts, x.data_ptr(),
+                                  _DT[x.dtype], max(x.stride(0), self.hidden), T, ids.data_ptr(), w.data_ptr(), k,
+                                  _ptr(self.x_scale), _ptr(self.h_scale), out.data_ptr(), _DT[dtype],
+                                  self._ws.data_ptr(), self._ws.numel(), _raw_stream(stream, dev.index))
+        if st:
+            check(st, "hq_fp4_experts")
         return out
 
     def check_status(self, stream=None):

@@ -33,6 +33,14 @@ def _raw_stream(stream, device_index):
     return get(device_index) if get is not None else torch.cuda.current_stream().cuda_stream
 
 
+def _on_device(dev, fn, *args):
+    """fn(*args) with dev as the current device (left alone where it already is)."""
+    if dev.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:

@@ -6,21 +6,10 @@ here.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from ._lib import check, lib
-from .hq import _DT, _need_cuda, _ptr, _raw_stream
-
-
-def _on(t: torch.Tensor):
-    """The device of t as the current one, for the launches of a call."""
-    return torch.cuda.device(t.device)
-
-
-def _st(stream, t):
-    return _raw_stream(stream, t.device.index)
+from .hq import _DT, _need_cuda, _on_device, _raw_stream
 
 
 class MoePlan:
@@ -28,8 +17,16 @@ class MoePlan:
     without one), offsets int32 [n_experts + 1], counts int32 [n_experts];
     n_rows: rows that hold every possible routing of these sizes."""
 
-    def __init__(self, pos, offsets, counts, n_rows, align):
-        self.pos, self.offsets, self.counts, self.n_rows, self.align = pos, offsets, counts, n_rows, align
+    def __init__(self, pos, ends, n_experts, n_rows, align):
+        self.pos, self._ends, self.n_experts, self.n_rows, self.align = pos, ends, n_experts, n_rows, align
+
+    @property
+    def offsets(self):
+        return self._ends[:self.n_experts + 1]
+
+    @property
+    def counts(self):
+        return self._ends[self.n_experts + 1:]
 
 
 def hq_moe_sort(topk_ids: torch.Tensor, n_experts: int, align: int = 1, workspace: torch.Tensor | None = None,
@@ -40,28 +37,30 @@ def hq_moe_sort(topk_ids: torch.Tensor, n_experts: int, align: int = 1, workspac
     _need_cuda(topk_ids, workspace)
     if topk_ids.dtype != torch.int32 or topk_ids.dim() != 2 or not topk_ids.is_contiguous():
         raise ValueError("topk_ids must be a contiguous int32 [T][k] tensor")
-    T, k = topk_ids.shape
-    dev = topk_ids.device
-    with _on(topk_ids):
-        need = int(lib().hq_moe_sort_workspace_size(T, k, n_experts))
-        if workspace is None:
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        pos = torch.empty((T, k), dtype=torch.int32, device=dev)
-        ends = torch.empty(max(2 * n_experts + 1, 1), dtype=torch.int32, device=dev)
-        offsets, counts = ends[:n_experts + 1], ends[n_experts + 1:]
-        check(lib().hq_moe_sort(_ptr(topk_ids), T, k, n_experts, align, _ptr(pos), _ptr(offsets), _ptr(counts),
-                                _ptr(workspace), workspace.numel(), _st(stream, topk_ids)), "hq_moe_sort")
-    return MoePlan(pos, offsets, counts, T * k + min(n_experts, T * k) * (align - 1), align)
+    return _on_device(topk_ids.device, _sort, topk_ids, int(n_experts), int(align), workspace, stream)
+
+
+def _sort(ids, E, align, ws, stream):
+    dev, (T, k) = ids.device, ids.shape
+    if ws is None:
+        ws = torch.empty(max(int(lib().hq_moe_sort_workspace_size(T, k, E)), 256), dtype=torch.uint8, device=dev)
+    pos = torch.empty_like(ids)
+    ends = torch.empty(max(2 * E + 1, 1), dtype=torch.int32, device=dev)
+    p = ends.data_ptr()
+    st = lib().hq_moe_sort(ids.data_ptr(), T, k, E, align, pos.data_ptr(), p, p + 4 * (E + 1), ws.data_ptr(), ws.numel(),
+                           _raw_stream(stream, dev.index))
+    if st:
+        check(st, "hq_moe_sort")
+    return MoePlan(pos, ends, E, T * k + min(E, T * k) * (align - 1), align)
 
 
 def _need_like(t, what, shape, dtype, dev):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
         raise ValueError(f"{what} must be a contiguous {dtype} tensor {tuple(shape)} on {dev}")
 
 
 def _need_rows(x, what, plan, tokens):
     """x [T][H] (tokens) or [n_rows][H], of a type the kernels take, on the plan's device."""
-    _need_cuda(x, plan.pos)
     if x.dtype not in _DT or x.dim() != 2 or not x.is_contiguous() or x.device != plan.pos.device:
         raise ValueError(f"{what} must be a contiguous fp16, bf16 or fp32 matrix on the plan's device")
     if tokens and x.shape[0] != plan.pos.shape[0]:
@@ -76,14 +75,20 @@ def hq_moe_gather(x: torch.Tensor, plan: MoePlan, out: torch.Tensor | None = Non
     """Each token's row x[t] to the rows of its pairs: [n_rows][H] (rows without
     a pair are left as they are in `out`; a new tensor's are not initialised)."""
     _need_rows(x, "x", plan, True)
-    T, H = x.shape
+    H = x.shape[1]
     if out is None:
         out = torch.empty((plan.n_rows, H), dtype=x.dtype, device=x.device)
     else:
         _need_like(out, "out", (out.shape[0], H), x.dtype, x.device)
-    with _on(x):
-        check(lib().hq_moe_gather(_ptr(x), _DT[x.dtype], _ptr(plan.pos), T, plan.pos.shape[1], H, _ptr(out),
-                                  out.shape[0], _st(stream, x)), "hq_moe_gather")
+    return _on_device(x.device, _gather, x, plan, out, stream)
+
+
+def _gather(x, plan, out, stream):
+    T, k = plan.pos.shape
+    st = lib().hq_moe_gather(x.data_ptr(), _DT[x.dtype], plan.pos.data_ptr(), T, k, x.shape[1], out.data_ptr(),
+                             out.shape[0], _raw_stream(stream, x.device.index))
+    if st:
+        check(st, "hq_moe_gather")
     return out
 
 
@@ -98,9 +103,16 @@ def _combine(rows, plan, topk_w, out_dtype, out, stream):
         out = torch.empty((T, H), dtype=dt, device=rows.device)
     else:
         _need_like(out, "out", (T, H), dt, rows.device)
-    with _on(rows):
-        check(lib().hq_moe_combine(_ptr(rows), _DT[rows.dtype], rows.shape[0], _ptr(plan.pos), _ptr(topk_w), T, k, H,
-                                   _ptr(out), _DT[dt], _st(stream, rows)), "hq_moe_combine")
+    return _on_device(rows.device, _launch_combine, rows, plan, topk_w, out, stream)
+
+
+def _launch_combine(rows, plan, topk_w, out, stream):
+    T, k = plan.pos.shape
+    st = lib().hq_moe_combine(rows.data_ptr(), _DT[rows.dtype], rows.shape[0], plan.pos.data_ptr(),
+                              None if topk_w is None else topk_w.data_ptr(), T, k, rows.shape[1], out.data_ptr(),
+                              _DT[out.dtype], _raw_stream(stream, rows.device.index))
+    if st:
+        check(st, "hq_moe_combine")
     return out
 
 
@@ -129,16 +141,21 @@ def hq_moe_combine_grad(dy: torch.Tensor, rows: torch.Tensor, plan: MoePlan, top
     _need_weights(topk_w, plan)
     if rows.dtype != dy.dtype or rows.shape[1] != dy.shape[1]:
         raise ValueError("dy and rows must have one type and width")
-    T, H = dy.shape
     if out is None:
         out = torch.empty_like(rows)
     else:
         _need_like(out, "out", rows.shape, rows.dtype, rows.device)
-    dw = torch.empty(plan.pos.shape, dtype=torch.float32, device=dy.device)
-    with _on(dy):
-        check(lib().hq_moe_combine_grad(_ptr(dy), _DT[dy.dtype], _ptr(rows), rows.shape[0], _ptr(plan.pos),
-                                        _ptr(topk_w), T, plan.pos.shape[1], H, _ptr(out), _ptr(dw), _st(stream, dy)),
-              "hq_moe_combine_grad")
+    return _on_device(dy.device, _combine_grad, dy, rows, plan, topk_w, out, stream)
+
+
+def _combine_grad(dy, rows, plan, topk_w, out, stream):
+    T, k = plan.pos.shape
+    dw = torch.empty_like(topk_w)
+    st = lib().hq_moe_combine_grad(dy.data_ptr(), _DT[dy.dtype], rows.data_ptr(), rows.shape[0], plan.pos.data_ptr(),
+                                   topk_w.data_ptr(), T, k, rows.shape[1], out.data_ptr(), dw.data_ptr(),
+                                   _raw_stream(stream, dy.device.index))
+    if st:
+        check(st, "hq_moe_combine_grad")
     return out, dw
 
 
