@@ -141,7 +141,7 @@ def lib() -> ctypes.CDLL:
         L.hq_fp4_linear_workspace_size.restype = _sz
         L.hq_fp4_linear.argtypes = [pm, _vp, _i, _sz, _i, _vp, _vp, _i, _sz, _vp, _sz, _vp]
         L.hq_fp4_linear.restype = _i
-        L.hq_fp4_linear_launches.argtypes = []
+        L.hq_fp4_linear_launches.argtypes = [pm, _i]
         L.hq_fp4_linear_launches.restype = _i
         L.hq_fp4_experts_workspace_size.argtypes = [pm, pm, pm, _i, _i, _i, _i]
         L.hq_fp4_experts_workspace_size.restype = _sz

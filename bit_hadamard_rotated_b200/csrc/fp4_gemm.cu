@@ -52,6 +52,8 @@ constexpr int kChunk = 256;  // values of K per ring slot (128 bytes a row)
 constexpr int kWBytes = kM * kChunk / 2;
 constexpr int kTurnRow = 36;  // floats per token of an epilogue transpose (32 and padding)
 constexpr int kMaxGroups = 1024;
+constexpr int kMaxEpiWarps = 8;   // of a kernel that splits tiles
+constexpr int kFusedTokens = 8;   // most tokens of a fused launch (one swizzle atom)
 constexpr int kSmemMax = 218 * 1024;  // dynamic; the experts' segments (12 KB) beside it
 
 // ------------------------------------------------------------------ PTX
@@ -118,9 +120,10 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
 
 // ------------------------------------------------------------------ plan
 
-// What a launch computes: y of one matrix; y of every expert's rows; or the
-// quantised h = silu(gate) up of every expert's rows.
-enum Mode { kDense = 0, kGrouped = 1, kGated = 2 };
+// What a launch computes: y of one matrix; y of every expert's rows; the
+// quantised h = silu(gate) up of every expert's rows; or y of one matrix for a
+// few real-valued tokens, quantised on the way.
+enum Mode { kDense = 0, kGrouped = 1, kGated = 2, kFused = 3 };
 
 template <int FMT, int NT, int MODE>
 struct Shape {
@@ -128,19 +131,20 @@ struct Shape {
   static constexpr int kTiles = kChunk / (FMT == HQ_FP4_NV ? 64 : 128);  // scale tiles per chunk
   static constexpr int kSf = kTiles * 512;                               // one row tile's scales
   static constexpr int kRowTiles = NT > 128 ? NT / 128 : 1;              // token scale tiles
-  static constexpr int kABytes = NT * kChunk / 2;
+  static constexpr int kABytes = MODE == kFused ? 0 : NT * kChunk / 2;
   static constexpr int kSfOff = kW * kWBytes + kABytes;                  // scales: weights', then tokens'
-  static constexpr int kSlot = kSfOff + (kW + kRowTiles) * kSf;
+  static constexpr int kSlot = kSfOff + (MODE == kFused ? kW : kW + kRowTiles) * kSf;
   static constexpr int kAccs = kW * NT <= 128 ? 2 : 1;                   // accumulator sets
   static constexpr int kSfCols = kTiles * 4 * (kW + kRowTiles);          // one slot's scales
-  static constexpr int kEpiWarps = 8;
-  static constexpr int kThreads = 64 + 32 * kEpiWarps;
+  static constexpr bool kGroups = MODE == kGrouped || MODE == kGated;
+  static constexpr int kTokWarps = MODE == kFused ? 4 : 0;               // quantise tokens beside the epilogue's
+  static constexpr int kEpiWarps = MODE == kFused ? 4 : MODE == kGated && NT > 64 ? 16 : 8;
+  static constexpr int kThreads = 64 + 32 * (kTokWarps + kEpiWarps);
   static constexpr int kTurn = MODE == kGated ? kEpiWarps * 16 * kTurnRow * 4 : 0;  // epilogue transposes
-  static constexpr int kFit = (kSmemMax - kTurn - 2048 - (MODE == kDense ? 0 : 4096)) / kSlot;
+  static constexpr int kFit = (kSmemMax - kTurn - 2048 - (kGroups ? 4096 : 0)) / kSlot;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kColsNeeded = kAccs * kW * NT + 2 * kSfCols;
   static constexpr int kCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kSlot + kTurn + 512;
   static_assert(kColsNeeded <= 512, "tensor memory");
   static_assert(kSlot % 1024 == 0, "swizzle atoms");
 };
@@ -175,7 +179,24 @@ struct GemmArgs {
   uint8_t* h_scales;
   int h_kb;
   int early;           // the weights may be read before the preceding kernel ends
+  // fused: the tokens
+  const void* x;
+  int x_dtype;
+  size_t ldx;
+  int K;
+  int stages;          // ring slots (beside them, the tokens of all of K)
 };
+
+// Fused: shared memory of a chunk's tokens, 8 rows: codes (one swizzle atom)
+// and scale cells (8 rows x 16 bytes per tile; tcgen05.cp takes 512 bytes, the
+// rest is the following tiles' and ends in lanes that no MMA reads).
+constexpr int kTokenCodes = 1024;
+template <int FMT>
+constexpr int kTokenScales = (FMT == HQ_FP4_NV ? 4 : 2) * 128;
+template <int FMT>
+constexpr size_t token_bytes(int chunks) {
+  return static_cast<size_t>(chunks + 1) * kTokenCodes + (static_cast<size_t>(chunks) * kTokenScales<FMT> + 1023) / 1024 * 1024 + 1024;
+}
 
 // One item of a CTA's list: a tile and its chunks [c0, c1).
 struct Item {
@@ -314,6 +335,19 @@ __device__ __forceinline__ void store_any(const GemmArgs& a, size_t row, int m, 
   else store_column<P>(static_cast<float*>(a.y) + o, a.ldy, f, n);
 }
 
+// 16 values of token `row` from `col` on (0 outside).
+__device__ __forceinline__ void load_token(const GemmArgs& a, int row, int col, float (&v)[16]) {
+  if (row < a.N && col < a.K) {
+    const size_t o = row * a.ldx + col;
+    if (a.x_dtype == HQ_BF16) load_chunk<__nv_bfloat16, 16>(static_cast<const __nv_bfloat16*>(a.x) + o, v);
+    else if (a.x_dtype == HQ_F16) load_chunk<__half, 16>(static_cast<const __half*>(a.x) + o, v);
+    else load_chunk<float, 16>(static_cast<const float*>(a.x) + o, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  }
+}
+
 // P (16 or 32) accumulator columns from c on.
 template <int P>
 __device__ __forceinline__ void load_columns(uint32_t d, float (&f)[P]) {
@@ -336,18 +370,21 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wmap2,
                 const __grid_constant__ CUtensorMap amap, const GemmArgs a) {
   using S = Shape<FMT, NT, MODE>;
-  constexpr bool GROUPED = MODE != kDense;
-  constexpr int ST = S::kStages;
+  constexpr bool GROUPED = S::kGroups;
+  constexpr bool FUSED = MODE == kFused;
+  const int ST = FUSED ? a.stages : S::kStages;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   float* turn_buf = reinterpret_cast<float*>(ring + ST * S::kSlot);
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + ST * S::kSlot + S::kTurn);
+  uint8_t* tok = ring + ST * S::kSlot;  // fused: the tokens' codes, then their scales
+  uint8_t* tok_sf = tok + (a.C + 1) * kTokenCodes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + ST * S::kSlot +
+                                               (FUSED ? token_bytes<FMT>(a.C) : static_cast<size_t>(S::kTurn)));
   uint64_t* empty = full + ST;
   uint64_t* dfull = empty + ST;
   uint64_t* dempty = dfull + S::kAccs;
-  uint64_t* epi = dempty + S::kAccs;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(epi + 1);
-  uint32_t* flag = tslot + 1;
+  uint64_t* tok_full = dempty + S::kAccs;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(tok_full + 1);
   __shared__ int first[GROUPED ? 3 * kMaxGroups + 1 : 1];
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -359,11 +396,11 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       mbar_init(dfull + i, 1);
       mbar_init(dempty + i, S::kEpiWarps);
     }
-    mbar_init(epi, S::kEpiWarps);
+    mbar_init(tok_full, S::kTokWarps + S::kEpiWarps);
     fence_mbar_init();
     prefetch_tensormap(&wmap);
     if (MODE == kGated) prefetch_tensormap(&wmap2);
-    prefetch_tensormap(&amap);
+    if (!FUSED) prefetch_tensormap(&amap);
   }
   if (warp == 1) {
     tc::tmem_alloc(tslot, S::kCols);
@@ -376,13 +413,12 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   const uint32_t sf_cols = tmem + S::kAccs * S::kW * NT;
   if constexpr (GROUPED) {
     pdl_wait();  // the segments come from the sort
+    pdl_launch_dependents();
     load_groups<NT>(a, first);
   }
   bool ok = true;
 
   if (warp == 0) {
-    const bool early = !GROUPED && a.early != 0;
-    if (!GROUPED && !early) pdl_wait();
     Walk<NT, GROUPED> w(a, first);
     Item it;
     int slot = 0, turn = 0;
@@ -394,8 +430,8 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       Sizes z;
       z.tiles = min(S::kTiles, a.wkb - c * S::kTiles);
       z.row_tiles = min(S::kRowTiles, a.a_row_tiles - (t.n0 >> 7));
-      z.a_rows = GROUPED ? (t.n_valid + 15) / 16 * 16 : NT;
-      z.bytes = static_cast<uint32_t>(S::kW * kWBytes + z.a_rows * 128 + z.tiles * 512 * (S::kW + z.row_tiles));
+      z.a_rows = FUSED ? 0 : GROUPED ? (t.n_valid + 15) / 16 * 16 : NT;
+      z.bytes = static_cast<uint32_t>(S::kW * kWBytes + z.a_rows * 128 + z.tiles * 512 * (S::kW + (FUSED ? 0 : z.row_tiles)));
       return z;
     };
     auto weights = [&](const Item& t, int c, int s, const Sizes& z) {
@@ -433,12 +469,17 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     // With early weights the first ring of weight copies goes out before the
     // wait for the preceding kernel, the token copies of those slots after it.
     int ahead = 0;
-    if (early) {
+    if constexpr (!GROUPED) {
       Walk<NT, GROUPED> w2 = w;
-      while (ahead < ST && w2.next(a, it)) {
-        for (int c = it.c0; c < it.c1 && ahead < ST; ++c, ++ahead) weights(it, c, ahead, sizes(it, c));
+      if (a.early != 0) {
+        while (ahead < ST && w2.next(a, it)) {
+          for (int c = it.c0; c < it.c1 && ahead < ST; ++c, ++ahead) weights(it, c, ahead, sizes(it, c));
+        }
       }
       pdl_wait();
+      // After the wait, so that whatever precedes this kernel is complete when
+      // the next one starts.
+      pdl_launch_dependents();
     }
     int n = 0;  // chunks so far
     while (ok && w.next(a, it)) {
@@ -449,7 +490,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         }
         const Sizes z = sizes(it, c);
         if (n >= ahead) weights(it, c, slot, z);
-        tokens(it, c, slot, z);
+        if constexpr (!FUSED) tokens(it, c, slot, z);
         ++n;
         if (++slot == ST) {
           slot = 0;
@@ -457,12 +498,13 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         }
       }
     }
-    pdl_launch_dependents();
   } else if (warp == 1) {
     const uint32_t d0 = uniform(tmem), sf0 = uniform(sf_cols), ring0 = uniform(smem_u32(ring));
     Walk<NT, GROUPED> w(a, first);
     Item it;
     int slot = 0, par = 0, acc = 0, accn = 0, n = 0;
+    if (FUSED) ok = warp_wait(tok_full, 0);
+    const uint32_t tok0 = uniform(smem_u32(tok)), tok_sf0 = uniform(smem_u32(tok_sf));
     while (ok && w.next(a, it)) {
       const uint32_t d = d0 + acc * S::kW * NT;
       if (accn >= S::kAccs && !warp_wait(dempty + acc, (accn / S::kAccs - 1) & 1)) {
@@ -481,7 +523,8 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         tc::tc_fence_after();
         const uint32_t p = ring0 + slot * S::kSlot;
         const uint32_t sfa = sf0 + (n & 1) * S::kSfCols, sfb = sfa + S::kW * S::kTiles * 4, sp = p + S::kSfOff;
-        const uint64_t da = desc_sw128(p), db = desc_sw128(p + S::kW * kWBytes);
+        const uint64_t da = desc_sw128(p), db = desc_sw128(FUSED ? tok0 + c * kTokenCodes : p + S::kW * kWBytes);
+        const uint32_t sp_tok = FUSED ? tok_sf0 + c * kTokenScales<FMT> : sp + S::kW * S::kSf;
         const int steps = min(4, a.k_steps - 4 * c);
         const uint32_t first_sum = c > it.c0 ? 1u : 0u;
         ++n;
@@ -492,7 +535,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
             for (int i = 0; i < S::kW; ++i) tc_copy_scales(sfa + 4 * (i * S::kTiles + t), sp + i * S::kSf + 512 * t);
 #pragma unroll
             for (int r = 0; r < S::kRowTiles; ++r) {
-              tc_copy_scales(sfb + 4 * (t * S::kRowTiles + r), sp + S::kSf * (S::kW + r) + 512 * t);
+              tc_copy_scales(sfb + 4 * (t * S::kRowTiles + r), sp_tok + S::kSf * r + (FUSED ? 128 : 512) * t);
             }
           }
 #pragma unroll
@@ -520,21 +563,58 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     }
   } else {
     if constexpr (!GROUPED) pdl_wait();
-    const int ew = warp - 2, quarter = warp & 3;
+    if constexpr (FUSED) {
+      // All of the tokens, once per CTA, while the first weights are on their
+      // way: a thread takes 16 values, two loads ahead of each other.
+      constexpr int kWorkers = 32 * (S::kTokWarps + S::kEpiWarps);
+      const float ts = a.ats != nullptr ? __ldg(a.ats) : 1.f;
+      const int per_row = a.C * (kChunk / 16);
+      struct At {
+        int row, b;  // 16-value piece b of a row
+      };
+      auto step = [&](At& t) {
+        t.b += kWorkers;
+        while (t.b >= per_row) {
+          t.b -= per_row;
+          ++t.row;
+        }
+      };
+      auto pack = [&](const At& t, float (&v)[16]) {  // all lanes; rows and workers are multiples of 16 pieces
+        const Packed16 q = pack16<FMT>(v, ts, 1);
+        if (t.row >= a.N) return;
+        const int c = t.b >> 4, blk = t.b & 15;
+        // 128 bytes a row, 16-byte pieces exchanged by the row's place in its group of 8
+        *reinterpret_cast<uint2*>(tok + c * kTokenCodes + t.row * 128 + (((blk >> 1) ^ t.row) << 4) + (blk & 1) * 8) = q.codes;
+        constexpr int kPer = FMT == HQ_FP4_NV ? 1 : 2;  // threads per block
+        tok_sf[c * kTokenScales<FMT> + blk / (4 * kPer) * 128 + t.row * 16 + (blk / kPer & 3)] = static_cast<uint8_t>(q.byte);
+      };
+      At t0{0, static_cast<int>(threadIdx.x) - 64 - kWorkers}, t1;
+      float v0[16], v1[16];
+      step(t0);
+      load_token(a, t0.row, t0.b * 16, v0);
+      while (__any_sync(~0u, t0.row < a.N)) {
+        t1 = t0;
+        step(t1);
+        load_token(a, t1.row, t1.b * 16, v1);
+        pack(t0, v0);
+        t0 = t1;
+        step(t0);
+        load_token(a, t0.row, t0.b * 16, v0);
+        pack(t1, v1);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tok_full);
+    }
+    if (warp >= 2 + S::kTokWarps) {
+    const int ew = warp - 2 - S::kTokWarps, quarter = warp & 3;
     constexpr int kParts = S::kEpiWarps / 4;  // warps that share a lane quarter split the columns
     const int col0 = (ew >> 2) * (NT / kParts), col1 = col0 + NT / kParts;
     const int mrow = quarter * 32 + lane;
     const float ats = a.ats != nullptr ? __ldg(a.ats) : 1.f;
     Walk<NT, GROUPED> w(a, first);
     Item it;
-    int acc = 0, accn = 0, epar = 0;
-    auto meet = [&]() {  // all epilogue warps, bounded
-      __syncwarp();
-      if (lane == 0) mbar_arrive(epi);
-      const bool r = warp_wait(epi, epar);
-      epar ^= 1;
-      return r;
-    };
+    int acc = 0, accn = 0;
     while (ok && w.next(a, it)) {
       if (!warp_wait(dfull + acc, (accn / S::kAccs) & 1)) {
         ok = false;
@@ -551,17 +631,25 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         const float alpha2 = (a.wts2 != nullptr ? __ldg(a.wts2 + (a.n_wts2 > 1 ? it.e : 0)) : 1.f) * ats;
         const float hts = a.hts != nullptr ? __ldg(a.hts) : 1.f;
         float* buf = turn_buf + ew * 16 * kTurnRow;
-        for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
-          uint32_t g[16], u[16];
-          tc::tc_ld16(d + c, g);
-          tc::tc_ld16(d + NT + c, u);
-          tc::tc_wait_ld();
-          tc::tc_tie16(g);
-          tc::tc_tie16(u);
+        // All of the warp's columns first, so that the next tile's MMAs can have
+        // the accumulators while h is computed and packed.
+        constexpr int kCols = NT / kParts;
+        float g[kCols], u[kCols];
+        if (col0 < it.n_valid) {
+          load_columns<kCols>(d + col0, g);
+          load_columns<kCols>(d + NT + col0, u);
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dempty + acc);
+#pragma unroll
+        for (int c1 = 0; c1 < kCols; c1 += 16) {
+          const int c = col0 + c1;
+          if (c >= it.n_valid) break;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float x = __uint_as_float(g[i]) * alpha;
-            buf[i * kTurnRow + lane] = __fdividef(x, 1.f + __expf(-x)) * (__uint_as_float(u[i]) * alpha2);
+            const float x = g[c1 + i] * alpha;
+            buf[i * kTurnRow + lane] = __fdividef(x, 1.f + __expf(-x)) * (u[c1 + i] * alpha2);
           }
           __syncwarp();
           const int tok = lane & 15, part = lane >> 4;
@@ -588,9 +676,6 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
           }
           __syncwarp();
         }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(dempty + acc);
       } else if (whole) {
         constexpr int P = NT / kParts < 32 ? 16 : 32;
         for (int c = col0; c < col1 && c < it.n_valid; c += P) {
@@ -605,12 +690,12 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(dempty + acc);
-      } else if constexpr (MODE == kDense) {
+      } else if constexpr (!GROUPED) {
         // a tile shared by CTAs i0 .. i1: the units [t C, t C + C)
         const int t = (it.m0 / kM) * a.nt + it.n0 / NT;
-        const long first = static_cast<long>(t) * a.C, last = first + a.C - 1;
-        const int i0 = static_cast<int>(((first + 1) * gridDim.x - 1) / a.units);
-        const int i1 = static_cast<int>(((last + 1) * gridDim.x - 1) / a.units);
+        const long u0 = static_cast<long>(t) * a.C, u1 = u0 + a.C - 1;
+        const int i0 = static_cast<int>(((u0 + 1) * gridDim.x - 1) / a.units);
+        const int i1 = static_cast<int>(((u1 + 1) * gridDim.x - 1) / a.units);
         const size_t part_size = static_cast<size_t>(NT) * kM;
         // a CTA's second slot is for the tile that it begins
         float* mine = a.part + (2 * static_cast<size_t>(blockIdx.x) + (it.c0 == 0 ? 1 : 0)) * part_size;
@@ -621,23 +706,19 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
           for (int i = 0; i < 16; ++i) __stcg(mine + (c + i) * kM + mrow, f[i]);
         }
         tc::tc_fence_before();
-        __threadfence();
         __syncwarp();
         if (lane == 0) mbar_arrive(dempty + acc);
-        if (!meet()) {
-          ok = false;
-          break;
-        }
-        if (ew == 0 && lane == 0) {
+        // Each warp's share of the tile is counted on its own: the last of the
+        // tile's CTAs to bring it adds the parts.
+        uint32_t last = 0;
+        uint32_t* counter = a.counters + i0 * kMaxEpiWarps + ew;
+        if (lane == 0 && col0 < it.n_valid) {
           __threadfence();
-          *flag = atomicAdd(a.counters + i0, 1u) == static_cast<uint32_t>(i1 - i0) ? 1u : 0u;
+          last = atomicAdd(counter, 1u) == static_cast<uint32_t>(i1 - i0) ? 1u : 0u;
         }
-        if (!meet()) {
-          ok = false;
-          break;
-        }
-        if (*reinterpret_cast<volatile uint32_t*>(flag) != 0) {
+        if (__shfl_sync(~0u, last, 0) != 0) {
           __threadfence();
+          if (lane == 0) *counter = 0;
           for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
             float f[16];
 #pragma unroll
@@ -656,13 +737,11 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
               store_any<16>(a, it.n0 + c, m, f, it.n_valid - c);
             }
           }
-          if (ew == 0 && lane == 0) a.counters[i0] = 0;
         }
-        // the flag is read before it is written again: the next tile's first
-        // meeting comes between
       }
       ++accn;
       acc = accn % S::kAccs;
+    }
     }
   }
   if (!ok) record_error(a.status, HQ_DEV_TIMEOUT);
@@ -675,8 +754,8 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
 // ------------------------------------------------------------------ host
 
 constexpr size_t kStatusBytes = 256;
-constexpr size_t kCounterBytes = 1024;  // one word per CTA of a split grid
-constexpr int kMaxGrid = static_cast<int>(kCounterBytes / 4);
+constexpr size_t kCounterBytes = 8192;  // a word per epilogue warp and CTA of a split grid
+constexpr int kMaxGrid = static_cast<int>(kCounterBytes / 4 / kMaxEpiWarps);
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
@@ -717,8 +796,35 @@ template <int FMT, int NT, int MODE>
 cudaError_t gemm_launch(const CUtensorMap& wmap, const CUtensorMap& wmap2, const CUtensorMap& amap,
                         const GemmArgs& a, int grid, cudaStream_t st) {
   using S = Shape<FMT, NT, MODE>;
-  return launch_pdl(gemm_kernel<FMT, NT, MODE>, dim3(grid), dim3(S::kThreads), S::kSmem, st, true, wmap, wmap2, amap,
+  const size_t smem = 1024 + static_cast<size_t>(S::kStages) * S::kSlot + S::kTurn + 512;
+  return launch_pdl(gemm_kernel<FMT, NT, MODE>, dim3(grid), dim3(S::kThreads), smem, st, true, wmap, wmap2, amap,
                     a);
+}
+
+// Ring slots of a fused launch beside the tokens of C chunks (0: no room).
+template <int FMT>
+int fused_stages(int C) {
+  using S = Shape<FMT, 32, kFused>;
+  const long room = kSmemMax - 2048 - static_cast<long>(token_bytes<FMT>(C));
+  const long n = room / S::kSlot;
+  return n < 4 ? 0 : static_cast<int>(std::min<long>(n, 8));
+}
+// One launch or two: every CTA quantises all of the tokens, 1.7 us per 8192
+// values, a kernel of its own costs about 2.5 us.  28672 x 8192: one token 27.5
+// against 30.2 us, two 30.2 against 29.9, eight 40 against 30; 4096 x 4096: two
+// tokens 9.5 against 11.4, eight 13.1 against 11.3.
+bool fused_fits(int fmt, int N, int K) {
+  const int C = (K + kChunk - 1) / kChunk;
+  return N <= kFusedTokens && static_cast<long>(N) * K <= 8192 &&
+         (fmt == HQ_FP4_NV ? fused_stages<HQ_FP4_NV>(C) : fused_stages<HQ_FP4_MX>(C)) > 0;
+}
+
+template <int FMT>
+cudaError_t fused_launch(const CUtensorMap& wmap, GemmArgs& a, int grid, cudaStream_t st) {
+  using S = Shape<FMT, 32, kFused>;
+  a.stages = fused_stages<FMT>(a.C);
+  const size_t smem = 1024 + static_cast<size_t>(a.stages) * S::kSlot + token_bytes<FMT>(a.C) + 512;
+  return launch_pdl(gemm_kernel<FMT, 32, kFused>, dim3(grid), dim3(S::kThreads), smem, st, true, wmap, wmap, wmap, a);
 }
 
 template <int FMT>
@@ -745,22 +851,13 @@ cudaError_t code_map(CUtensorMap* map, const uint8_t* codes, long rows, int K, i
                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// y = W a for a packed token matrix; part and counters as the plan needs them.
-cudaError_t launch_matmul(const hq_fp4_matrix* w, const uint8_t* codes, const uint8_t* scales, const float* ats,
-                          int N, void* y, hq_dtype yd, size_t ldy, uint8_t* ws, uint8_t* part, bool early,
-                          cudaStream_t st) {
-  const Plan p = plan_of(w->rows, N, w->K);
-  CUtensorMap wmap, amap;
-  cudaError_t e = code_map(&wmap, w->codes, w->rows, w->K, kM);
-  if (e != cudaSuccess) return e;
-  e = code_map(&amap, codes, N, w->K, p.nt_size);
-  if (e != cudaSuccess) return e;
+// What a dense product's launch takes from its weights and plan.
+GemmArgs dense_args(const hq_fp4_matrix* w, const Plan& p, int N, void* y, hq_dtype yd, size_t ldy, uint8_t* ws,
+                    uint8_t* part) {
   GemmArgs a{};
   a.wsf = w->scales;
-  a.asf = scales;
   a.wts = w->tensor_scale;
   a.n_wts = 1;
-  a.ats = ats;
   a.wkb = scale_tiles(w->format, w->K);
   a.a_row_tiles = (N + 127) / 128;
   a.M = w->rows;
@@ -776,6 +873,39 @@ cudaError_t launch_matmul(const hq_fp4_matrix* w, const uint8_t* codes, const ui
   a.status = reinterpret_cast<uint32_t*>(ws);
   a.counters = reinterpret_cast<uint32_t*>(ws + kStatusBytes);
   a.part = reinterpret_cast<float*>(part);
+  return a;
+}
+
+// y = W q(x) for a few tokens in one launch.
+cudaError_t launch_fused(const hq_fp4_matrix* w, const void* x, hq_dtype xd, size_t ldx, int N, const float* x_scale,
+                         void* y, hq_dtype yd, size_t ldy, uint8_t* ws, uint8_t* part, cudaStream_t st) {
+  const Plan p = plan_of(w->rows, N, w->K);
+  CUtensorMap wmap;
+  const cudaError_t e = code_map(&wmap, w->codes, w->rows, w->K, kM);
+  if (e != cudaSuccess) return e;
+  GemmArgs a = dense_args(w, p, N, y, yd, ldy, ws, part);
+  a.ats = x_scale;
+  a.x = x;
+  a.x_dtype = xd;
+  a.ldx = ldx;
+  a.K = w->K;
+  return w->format == HQ_FP4_NV ? fused_launch<HQ_FP4_NV>(wmap, a, p.grid, st)
+                                : fused_launch<HQ_FP4_MX>(wmap, a, p.grid, st);
+}
+
+// y = W a for a packed token matrix; part and counters as the plan needs them.
+cudaError_t launch_matmul(const hq_fp4_matrix* w, const uint8_t* codes, const uint8_t* scales, const float* ats,
+                          int N, void* y, hq_dtype yd, size_t ldy, uint8_t* ws, uint8_t* part, bool early,
+                          cudaStream_t st) {
+  const Plan p = plan_of(w->rows, N, w->K);
+  CUtensorMap wmap, amap;
+  cudaError_t e = code_map(&wmap, w->codes, w->rows, w->K, kM);
+  if (e != cudaSuccess) return e;
+  e = code_map(&amap, codes, N, w->K, p.nt_size);
+  if (e != cudaSuccess) return e;
+  GemmArgs a = dense_args(w, p, N, y, yd, ldy, ws, part);
+  a.asf = scales;
+  a.ats = ats;
   a.early = early ? 1 : 0;
   return w->format == HQ_FP4_NV ? dense_launch<HQ_FP4_NV>(p.nt_size, wmap, amap, a, p.grid, st)
                                 : dense_launch<HQ_FP4_MX>(p.nt_size, wmap, amap, a, p.grid, st);
@@ -985,6 +1115,9 @@ hq_status hq_fp4_linear(const hq_fp4_matrix* w, const void* x, hq_dtype x_dtype,
   uint8_t* codes = ws + fp4::kStatusBytes + fp4::kCounterBytes;
   uint8_t* scales = codes + fp4::align256(static_cast<size_t>(batch) * (w->K / 2));
   uint8_t* part = scales + fp4::align256(fp4::scale_bytes(w->format, batch, w->K));
+  if (fp4::fused_fits(w->format, batch, w->K)) {
+    return from_cuda(fp4::launch_fused(w, x, x_dtype, ldx, batch, x_scale, y, y_dtype, ldy, ws, part, st));
+  }
   const cudaError_t e = fp4::launch_quantize(w->format, x_dtype, x, ldx, batch, w->K, x_scale, codes, scales,
                                              nullptr, nullptr, 1, batch, st);
   if (e != cudaSuccess) return from_cuda(e);
@@ -994,7 +1127,10 @@ hq_status hq_fp4_linear(const hq_fp4_matrix* w, const void* x, hq_dtype x_dtype,
   return from_cuda(fp4::launch_matmul(w, codes, scales, x_scale, batch, y, y_dtype, ldy, ws, part, true, st));
 }
 
-int hq_fp4_linear_launches(void) { return 2; }
+int hq_fp4_linear_launches(const hq_fp4_matrix* w, int batch) {
+  if (fp4::check_matrix(w) != HQ_OK || batch < 1) return 0;
+  return fp4::fused_fits(w->format, batch, w->K) ? 1 : 2;
+}
 
 size_t hq_fp4_experts_workspace_size(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, const hq_fp4_matrix* down,
                                      int n_experts, int T, int k, hq_dtype y_dtype) {

@@ -62,25 +62,9 @@ struct QuantArgs {
 
 
 template <typename T, int FMT>
-__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs a) {
-  pdl_wait();
-  pdl_launch_dependents();
-  // Rows from the last to the first: what wrote x, or read it for its largest
-  // value, did the end last, and that part may still lie in L2.
-  const int r = static_cast<int>(threadIdx.x * a.inv >> 16);
-  const int cb = threadIdx.x - r * a.cpb;
-  const long row = static_cast<long>(gridDim.x - 1 - blockIdx.x) * a.rpb + r;
-  const int c = blockIdx.y * a.cpb + cb;
-  const bool mine = r < a.rpb && c < a.c_pad;
+__device__ __forceinline__ void quantize_piece(const QuantArgs& a, long row, int c, bool mine, float ts,
+                                               float (&v)[16]) {
   const bool live = mine && row < a.rows && c * 16 < a.K;
-  float v[16];
-  if (live) {
-    load_chunk<T, 16>(static_cast<const T*>(a.x) + row * a.ldx + c * 16, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
-  }
-  const float ts = FMT == HQ_FP4_NV && a.ts != nullptr ? __ldg(a.ts) : 1.f;
   const Packed16 p = pack16<FMT>(v, ts, 1);
   const uint32_t byte = live ? p.byte : 0u;
   // four blocks' scales in one word
@@ -110,6 +94,27 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
       if (scale_lane) *reinterpret_cast<uint32_t*>(a.scales + scale_cell(dst, st, a.kb)) = sw;
     }
   }
+}
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  // Rows from the last to the first: what wrote x, or read it for its largest
+  // value, did the end last, and that part may still lie in L2.
+  const int r = static_cast<int>(threadIdx.x * a.inv >> 16);
+  const int c = blockIdx.y * a.cpb + threadIdx.x - r * a.cpb;
+  const long row = static_cast<long>(gridDim.x - 1 - blockIdx.x) * a.rpb + r;
+  const bool mine = r < a.rpb && c < a.c_pad;
+  const float ts = FMT == HQ_FP4_NV && a.ts != nullptr ? __ldg(a.ts) : 1.f;
+  float v[16];
+  if (mine && row < a.rows && c * 16 < a.K) {
+    load_chunk<T, 16>(static_cast<const T*>(a.x) + row * a.ldx + c * 16, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = 0.f;
+  }
+  quantize_piece<T, FMT>(a, row, c, mine, ts, v);
 }
 
 // The largest magnitude of a tensor over 2688 (= 6 * 448, the largest value

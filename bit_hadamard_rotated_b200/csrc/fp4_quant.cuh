@@ -78,19 +78,20 @@ __device__ __forceinline__ void quotients(float (&v)[16], float eff) {
   }
 }
 
-// Eight values to eight E2M1 codes (low nibble first), round to nearest even,
-// saturating.
-__device__ __forceinline__ uint32_t to_e2m1x8(const float* v) {
+// Two values to two E2M1 codes (low nibble first), round to nearest even,
+// saturating.  One conversion per statement: four with their bytes packed by a
+// vector mov in one statement were compiled to zeros in one of the kernels
+// (CUDA 12.9; its test is the equality of the fused and the two-step product).
+__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
   uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
       : "=r"(r)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+      : "f"(hi), "f"(lo));
   return r;
+}
+__device__ __forceinline__ uint32_t to_e2m1x8(const float* v) {
+  return to_e2m1x2(v[0], v[1]) | to_e2m1x2(v[2], v[3]) << 8 | to_e2m1x2(v[4], v[5]) << 16 |
+         to_e2m1x2(v[6], v[7]) << 24;
 }
 
 __device__ __forceinline__ float2 from_e2m1x2(uint32_t b) {

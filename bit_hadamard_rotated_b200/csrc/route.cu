@@ -22,7 +22,8 @@ namespace route {
 namespace {
 
 constexpr int kSortThreads = 1024;
-constexpr int kMinTile = 2048;      // pairs per sorting block, at least
+constexpr int kOneTile = 8192;      // pairs that one block sorts alone
+constexpr int kMinTile = 2048;      // pairs per block of more
 constexpr int kMaxTiles = 64;       // blocks of one sort: each reads all blocks' histograms
 constexpr int kMaxExperts = 16384;
 constexpr long kMaxPairs = 1l << 23;
@@ -174,16 +175,17 @@ template <typename T, bool VEC>
 struct Piece {
   static constexpr int N = VEC ? 16 / sizeof(T) : 1;
   float v[N];
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (VEC) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-      const T* t = reinterpret_cast<const T*>(&u);
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = to_f32<T>(t[i]);
-    } else {
-      v[0] = to_f32<T>(*p);
-    }
+  using Raw = typename std::conditional<VEC, uint4, T>::type;
+  static __device__ __forceinline__ Raw raw(const T* p) {
+    if constexpr (VEC) return __ldg(reinterpret_cast<const uint4*>(p));
+    else return __ldg(p);
   }
+  __device__ __forceinline__ void unpack(const Raw& u) {
+    const T* t = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = to_f32<T>(t[i]);
+  }
+  __device__ __forceinline__ void load(const T* p) { unpack(raw(p)); }
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (VEC) {
       uint4 u;
@@ -233,26 +235,29 @@ __global__ void __launch_bounds__(256) combine_kernel(const MoveArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const size_t t = blockIdx.x;
-  constexpr int N = Piece<T, VEC>::N, U = 4;  // slots in flight
+  constexpr int N = Piece<T, VEC>::N, U = 8;  // slots in flight
   for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * N; c < a.H; c += gridDim.y * blockDim.x * N) {
     float s[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i] = 0.f;
     for (int j0 = 0; j0 < a.k; j0 += U) {
-      Piece<T, VEC> p[U];
+      typename Piece<T, VEC>::Raw p[U];
+      float w[U];
       bool ok[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = j0 + u < a.k ? __ldg(a.pos + t * a.k + j0 + u) : -1;
         ok[u] = static_cast<uint32_t>(r) < static_cast<uint32_t>(a.n_rows);
-        if (ok[u]) p[u].load(static_cast<const T*>(a.a) + static_cast<size_t>(r) * a.H + c);
+        if (ok[u]) p[u] = Piece<T, VEC>::raw(static_cast<const T*>(a.a) + static_cast<size_t>(r) * a.H + c);
+        if (WEIGHTED && ok[u]) w[u] = __ldg(a.w + t * a.k + j0 + u);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (!ok[u]) continue;
-        const float w = WEIGHTED ? __ldg(a.w + t * a.k + j0 + u) : 1.f;
+        Piece<T, VEC> x;
+        x.unpack(p[u]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = WEIGHTED ? fmaf(w, p[u].v[i], s[i]) : s[i] + p[u].v[i];
+        for (int i = 0; i < N; ++i) s[i] = WEIGHTED ? fmaf(w[u], x.v[i], s[i]) : s[i] + x.v[i];
       }
     }
     OutT* o = static_cast<OutT*>(a.out) + t * a.H + c;
@@ -298,16 +303,31 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const MoveArgs a) {
     const T* z = static_cast<const T*>(a.b) + static_cast<size_t>(r) * a.H;
     T* dz = static_cast<T*>(a.out) + static_cast<size_t>(r) * a.H;
     const float w = __ldg(a.w + pair);
-#pragma unroll 4
-    for (int c = lane * N; c < a.H; c += 32 * N) {
-      Piece<T, VEC> g, x;
-      g.load(dy + c);
-      x.load(z + c);
+    constexpr int U = VEC ? 4 : 8;  // pieces of both rows in flight
+    for (int c0 = lane * N; c0 < a.H; c0 += 32 * N * U) {
+      typename Piece<T, VEC>::Raw rg[U], rx[U];
 #pragma unroll
-      for (int i = 0; i < N; ++i) dot = fmaf(g.v[i], x.v[i], dot);
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + 32 * N * u;
+        if (c < a.H) {
+          rg[u] = Piece<T, VEC>::raw(dy + c);
+          rx[u] = Piece<T, VEC>::raw(z + c);
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < N; ++i) g.v[i] *= w;
-      g.store(dz + c);
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + 32 * N * u;
+        if (c < a.H) {
+          Piece<T, VEC> g, x;
+          g.unpack(rg[u]);
+          x.unpack(rx[u]);
+#pragma unroll
+          for (int i = 0; i < N; ++i) dot = fmaf(g.v[i], x.v[i], dot);
+#pragma unroll
+          for (int i = 0; i < N; ++i) g.v[i] *= w;
+          g.store(dz + c);
+        }
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
@@ -342,6 +362,7 @@ cudaError_t by_type(hq_dtype d, F&& f) {
 }  // namespace
 
 static int sort_tile(long pairs) {
+  if (pairs <= kOneTile) return kOneTile;
   const long t = (pairs + kMaxTiles - 1) / kMaxTiles;
   return static_cast<int>(std::max<long>(kMinTile, (t + kMinTile - 1) / kMinTile * kMinTile));
 }
@@ -352,7 +373,7 @@ static int sort_tiles(long pairs) {
 
 // Room for every smaller number of pairs too.
 size_t sort_workspace_bytes(long pairs, int E) {
-  const long tiles = pairs > kMinTile ? std::min<long>(kMaxTiles, (pairs + kMinTile - 1) / kMinTile) : 0;
+  const long tiles = pairs > kOneTile ? std::min<long>(kMaxTiles, (pairs + kMinTile - 1) / kMinTile) : 0;
   return 256 + (static_cast<size_t>(tiles) * E * 4 + 255) / 256 * 256;
 }
 

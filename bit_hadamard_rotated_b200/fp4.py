@@ -145,8 +145,8 @@ def _out(out, rows, M, dtype, dev):
 
 def _workspace(ws, need, dev):
     if ws is None:
-        ws = torch.empty(max(need, 2048), dtype=torch.uint8, device=dev)
-        ws[:2048].zero_()  # the status word and the counters: all that has to be zero
+        ws = torch.empty(max(need, 8448), dtype=torch.uint8, device=dev)
+        ws[:8448].zero_()  # the status word and the counters: all that has to be zero
         return ws
     if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")

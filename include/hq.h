@@ -429,7 +429,7 @@ hq_status hq_fp4_tensor_scale(const void* x, hq_dtype x_dtype, size_t ldx, int r
 
 /* Bytes of workspace hq_fp4_matmul needs for n_rows rows of a (0 on a bad
  * argument); enough for fewer rows too.  Of a workspace of the hq_fp4 products
- * only the first 2048 bytes have to be zero before its first use. */
+ * only the first 8448 bytes have to be zero before its first use. */
 size_t hq_fp4_matmul_workspace_size(const hq_fp4_matrix* w, int n_rows);
 
 /*
@@ -454,8 +454,10 @@ hq_status hq_fp4_linear(const hq_fp4_matrix* w, const void* x, hq_dtype x_dtype,
                         const float* x_scale, void* y, hq_dtype y_dtype, size_t ldy, void* workspace,
                         size_t ws_bytes, hq_stream_t stream);
 
-/* Kernels one hq_fp4_linear call enqueues. */
-int hq_fp4_linear_launches(void);
+/* Kernels one hq_fp4_linear call enqueues: one for up to 8 tokens of together
+ * at most 8192 values (the product's CTAs quantise them), two beyond; 0 on a
+ * bad argument. */
+int hq_fp4_linear_launches(const hq_fp4_matrix* w, int batch);
 
 /* Bytes of workspace hq_fp4_experts needs (0 on a bad argument); enough for
  * fewer tokens too. */

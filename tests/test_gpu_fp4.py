@@ -65,7 +65,7 @@ def check_quantised(q, x, fmt, ts=None):
 
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("R,K", [(1, 32), (1, 8192), (3, 96), (33, 4128), (130, 160), (257, 1024), (5, 16384)])
+@pytest.mark.parametrize("R,K", [(1, 32), (1, 8192), (3, 96), (33, 4128), (130, 160), (257, 1024), (5, 16384), (2501, 4096), (20001, 288)])
 def test_quantize_bit_exact(fmt, dtype, R, K):
     x = rows(R, K, dtype, R + K)
     check_quantised(hq_fp4_quantize(x.cuda(), fmt, values=True), x, fmt)
