@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       // All of the tokens, once per CTA, while the first weights are on their
       // way: a thread takes 16 values, two loads ahead of each other.
       constexpr int kWorkers = 32 * (S::kTokWarps + S::kEpiWarps);
-      const float ts = a.ats != nullptr ? __ldg(a.ats) : 1.f;
+      const SixTs ts(a.ats);
       const int per_row = a.C * (kChunk / 16);
       struct At {
         int row, b;  // 16-value piece b of a row
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         }
       };
       auto pack = [&](const At& t, float (&v)[16]) {  // all lanes; rows and workers are multiples of 16 pieces
-        const Packed16 q = pack16<FMT>(v, ts, 1);
+        const Packed16 q = pack16<FMT>(v, top_of(v), ts, 1);
         if (t.row >= a.N) return;
         const int c = t.b >> 4, blk = t.b & 15;
         // 128 bytes a row, 16-byte pieces exchanged by the row's place in its group of 8
@@ -611,6 +611,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     constexpr int kParts = S::kEpiWarps / 4;  // warps that share a lane quarter split the columns
     const int col0 = (ew >> 2) * (NT / kParts), col1 = col0 + NT / kParts;
     const int mrow = quarter * 32 + lane;
+    const SixTs hts(MODE == kGated ? a.hts : nullptr);
     const float ats = a.ats != nullptr ? __ldg(a.ats) : 1.f;
     Walk<NT, GROUPED> w(a, first);
     Item it;
@@ -629,7 +630,6 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         // 16 tokens at a time: h of this lane's feature, a transpose through
         // shared memory, then 16 features of one token per lane
         const float alpha2 = (a.wts2 != nullptr ? __ldg(a.wts2 + (a.n_wts2 > 1 ? it.e : 0)) : 1.f) * ats;
-        const float hts = a.hts != nullptr ? __ldg(a.hts) : 1.f;
         float* buf = turn_buf + ew * 16 * kTurnRow;
         // All of the warp's columns first, so that the next tile's MMAs can have
         // the accumulators while h is computed and packed.
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
             const float4 f = *reinterpret_cast<const float4*>(buf + tok * kTurnRow + part * 16 + 4 * i);
             v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
           }
-          const Packed16 p = pack16<FMT>(v, hts, 16);
+          const Packed16 p = pack16<FMT>(v, top_of(v), hts, 16);
           const uint32_t other = __shfl_xor_sync(~0u, p.byte, 16);
           if (c + tok < it.n_valid) {
             const long row = it.n0 + c + tok;

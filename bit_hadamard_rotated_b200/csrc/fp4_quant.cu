@@ -62,10 +62,12 @@ struct QuantArgs {
 
 
 template <typename T, int FMT>
-__device__ __forceinline__ void quantize_piece(const QuantArgs& a, long row, int c, bool mine, float ts,
-                                               float (&v)[16]) {
+__device__ __forceinline__ void quantize_piece(const QuantArgs& a, long row, int c, bool mine, const SixTs& ts,
+                                               const Raw16<T>& raw) {
   const bool live = mine && row < a.rows && c * 16 < a.K;
-  const Packed16 p = pack16<FMT>(v, ts, 1);
+  float v[16];
+  raw.unpack(v);
+  const Packed16 p = pack16<FMT>(v, raw.top(), ts, 1);
   const uint32_t byte = live ? p.byte : 0u;
   // four blocks' scales in one word
   constexpr int S = FMT == HQ_FP4_NV ? 0 : 1;  // log2 of the threads per block
@@ -106,14 +108,13 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
   const int c = blockIdx.y * a.cpb + threadIdx.x - r * a.cpb;
   const long row = static_cast<long>(gridDim.x - 1 - blockIdx.x) * a.rpb + r;
   const bool mine = r < a.rpb && c < a.c_pad;
-  const float ts = FMT == HQ_FP4_NV && a.ts != nullptr ? __ldg(a.ts) : 1.f;
-  float v[16];
+  Raw16<T> v;
   if (mine && row < a.rows && c * 16 < a.K) {
-    load_chunk<T, 16>(static_cast<const T*>(a.x) + row * a.ldx + c * 16, v);
+    v.load(static_cast<const T*>(a.x) + row * a.ldx + c * 16);
   } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = 0.f;
+    v.zero();
   }
+  const SixTs ts(FMT == HQ_FP4_NV ? a.ts : nullptr);
   quantize_piece<T, FMT>(a, row, c, mine, ts, v);
 }
 

@@ -7,18 +7,48 @@
 #include <stdint.h>
 
 #include "hq_internal.h"
+#include "hq_io.cuh"
 
 namespace hq {
 namespace fp4 {
 
+// Whether 1 / b, and quotients by b, stay far from under- and overflow.
+__device__ __forceinline__ bool mid_range(float b) { return b >= 0x1p-100f && b <= 0x1p100f; }
+
+// x / b, correctly rounded, for x = 0 or of middling size like b and
+// y = 1 / b correctly rounded: Markstein's quotient correction (IBM J. Res.
+// Dev. 34, 1990).  q = x y is within an ulp, and q + (x - q b) y, both steps
+// fused, rounds to the correctly rounded quotient.
+__device__ __forceinline__ float quotient(float x, float b, float y) {
+  const float q = __fmul_rn(x, y);
+  return __fmaf_rn(__fmaf_rn(-q, b, x), y, q);
+}
+
+// 6 times the tensor scale and its reciprocal (NV).
+struct SixTs {
+  float ts, six, y;
+  bool mid;
+  __device__ __forceinline__ explicit SixTs(const float* p) {
+    if (p == nullptr) {
+      ts = 1.f, six = 6.f, y = 1.f / 6.f, mid = true;
+    } else {
+      ts = __ldg(p);
+      six = __fmul_rn(6.f, ts);
+      mid = mid_range(six);
+      y = mid ? __frcp_rn(six) : 0.f;
+    }
+  }
+};
+
 // The block scale of amax: the scale byte and its value times the tensor
 // scale.  In IEEE single precision, as the header defines it.
 template <int FMT>
-__device__ __forceinline__ void block_scale(float amax, float ts, uint32_t& byte, float& eff) {
+__device__ __forceinline__ void block_scale(float amax, const SixTs& t, uint32_t& byte, float& eff) {
   if constexpr (FMT == HQ_FP4_NV) {
-    byte = __nv_cvt_float_to_fp8(__fdiv_rn(amax, __fmul_rn(6.f, ts)), __NV_SATFINITE, __NV_E4M3);
+    const float v = t.mid && (amax == 0.f || mid_range(amax)) ? quotient(amax, t.six, t.y) : __fdiv_rn(amax, t.six);
+    byte = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
     const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3);
-    eff = __fmul_rn(__half2float(__half(h)), ts);
+    eff = __fmul_rn(__half2float(__half(h)), t.ts);
   } else {
     // floor(log2 amax) - 2, at least -127: the exponent field of a normal
     // amax less 2 (a subnormal amax gives the smallest scale either way)
@@ -49,15 +79,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 
 // x / eff for 16 values.  An E8M0 scale is a power of two and so is its
-// reciprocal (2^-125 to 2^127): one exact product.  Otherwise, where 1 / eff is
-// far from under- and overflow, by Markstein's quotient correction (IBM J. Res.
-// Dev. 34, 1990): with y the correctly rounded 1 / eff, q = x y is within an
-// ulp and q + (x - q eff) y, both steps fused, rounds to the correctly rounded
-// quotient; so ties between codes are met exactly, at 3 packed operations for
-// two values instead of two divisions.
+// reciprocal (2^-125 to 2^127): one exact product.  Otherwise as quotient()
+// above, two values at a time, so that ties between codes are met exactly at 3
+// packed operations instead of two divisions.
 template <int FMT>
 __device__ __forceinline__ void quotients(float (&v)[16], float eff) {
-  if (FMT == HQ_FP4_MX || (eff >= 0x1p-100f && eff <= 0x1p100f)) {
+  if (FMT == HQ_FP4_MX || mid_range(eff)) {
     const float yf = FMT == HQ_FP4_MX ? __uint_as_float(static_cast<uint32_t>(
                                             254 - max(static_cast<int>(__float_as_uint(eff) >> 23), 0)) << 23)
                                       : __frcp_rn(eff);
@@ -106,15 +133,20 @@ struct Packed16 {
   float eff;      // its value times the tensor scale
 };
 
-// 16 values of a block to codes and scale.  E8M0 blocks are two threads' 16
-// values, lanes `mate` apart (all lanes of the warp take part).
-template <int FMT>
-__device__ __forceinline__ Packed16 pack16(float (&v)[16], float ts, int mate) {
-  // The largest magnitude as a bit pattern: magnitudes order as their
-  // patterns, infinity and NaN lie above all finite ones.
+// The largest magnitude of 16 values, as its bit pattern: magnitudes order as
+// their patterns, infinity and NaN lie above all finite ones.
+__device__ __forceinline__ uint32_t top_of(const float (&v)[16]) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return top;
+}
+
+// 16 values of a block, largest magnitude `top`, to codes and scale.  E8M0
+// blocks are two threads' 16 values, lanes `mate` apart (all lanes of the warp
+// take part).
+template <int FMT>
+__device__ __forceinline__ Packed16 pack16(float (&v)[16], uint32_t top, const SixTs& ts, int mate) {
   if constexpr (FMT == HQ_FP4_MX) top = max(top, __shfl_xor_sync(~0u, top, mate));
   Packed16 p;
   block_scale<FMT>(__uint_as_float(top), ts, p.byte, p.eff);
@@ -129,6 +161,43 @@ __device__ __forceinline__ Packed16 pack16(float (&v)[16], float ts, int mate) {
   p.codes.y = to_e2m1x8(v + 8);
   return p;
 }
+
+// 16 consecutive values of a row as loaded.
+template <typename T>
+struct Raw16 {
+  static constexpr int N = sizeof(T);  // 16-byte vectors
+  uint4 u[N];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) u[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void unpack(float (&v)[16]) const {
+    const T* t = reinterpret_cast<const T*>(u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = to_f32<T>(t[i]);
+  }
+  // top_of, for 16-bit types two values at a time on their own patterns.
+  __device__ __forceinline__ uint32_t top() const {
+    if constexpr (sizeof(T) == 4) {
+      float v[16];
+      unpack(v);
+      return top_of(v);
+    } else {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+      uint32_t m = w[0] & 0x7FFF7FFFu;
+      m = __vmaxu2(m, w[1] & 0x7FFF7FFFu);
+#pragma unroll
+      for (int i = 2; i < 8; i += 2) m = __vimax3_u16x2(m, w[i] & 0x7FFF7FFFu, w[i + 1] & 0x7FFF7FFFu);
+      const uint32_t h = max(m & 0xFFFFu, m >> 16);
+      const unsigned short s = static_cast<unsigned short>(h);
+      return __float_as_uint(to_f32<T>(*reinterpret_cast<const T*>(&s)));
+    }
+  }
+};
 
 }  // namespace fp4
 }  // namespace hq
