@@ -13,10 +13,11 @@
 // One CTA walks a list of (tile, K range) items.  Per 256 values of K it needs
 // 16 KB of weight codes (one TMA box, 128-byte swizzle), the tokens' codes,
 // and the scale tiles (bulk copies), all on one mbarrier per ring slot.
-//   warp 0   producer: issues the copies
+//   warp 0   issues the weights' copies
 //   warp 1   moves the slot's scales to tensor memory (tcgen05.cp) and issues
 //            the MMAs (K = 64 each) behind them, in order; their commit frees
 //            the slot
+//   warp 2   issues the tokens' copies
 //   others   epilogue: tensor memory to registers, alpha, one rounding, y
 // The copies of the scales cost nothing beside the MMAs: 12 of them and 4 MMAs
 // of 256 tokens took 512 cycles, the MMAs' own time (through registers, by
@@ -139,7 +140,9 @@ struct Shape {
   static constexpr bool kGroups = MODE == kGrouped || MODE == kGated;
   static constexpr int kTokWarps = MODE == kFused ? 4 : 0;               // quantise tokens beside the epilogue's
   static constexpr int kEpiWarps = MODE == kFused ? 4 : MODE == kGated && NT > 64 ? 16 : 8;
-  static constexpr int kThreads = 64 + 32 * (kTokWarps + kEpiWarps);
+  static constexpr int kRoles = MODE == kFused ? 2 : 3;                  // warps that issue: weights, MMAs, tokens
+  static constexpr int kThreads = 32 * (kRoles + kTokWarps + kEpiWarps);
+  static constexpr int kBox = MODE == kDense ? NT : NT > 64 ? 64 : 16;   // token rows per copy
   static constexpr int kTurn = MODE == kGated ? kEpiWarps * 16 * kTurnRow * 4 : 0;  // epilogue transposes
   static constexpr int kFit = (kSmemMax - kTurn - 2048 - (kGroups ? 4096 : 0)) / kSlot;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(full + i, 1);
+      mbar_init(full + i, S::kRoles - 1);
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < S::kAccs; ++i) {
@@ -419,78 +422,68 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   bool ok = true;
 
   if (warp == 0) {
+    if (!GROUPED && a.early == 0) pdl_wait();
+    if (FUSED) pdl_launch_dependents();
     Walk<NT, GROUPED> w(a, first);
     Item it;
-    int slot = 0, turn = 0;
-    struct Sizes {
-      int tiles, row_tiles, a_rows;
-      uint32_t bytes;
-    };
-    auto sizes = [&](const Item& t, int c) {
-      Sizes z;
-      z.tiles = min(S::kTiles, a.wkb - c * S::kTiles);
-      z.row_tiles = min(S::kRowTiles, a.a_row_tiles - (t.n0 >> 7));
-      z.a_rows = FUSED ? 0 : GROUPED ? (t.n_valid + 15) / 16 * 16 : NT;
-      z.bytes = static_cast<uint32_t>(S::kW * kWBytes + z.a_rows * 128 + z.tiles * 512 * (S::kW + (FUSED ? 0 : z.row_tiles)));
-      return z;
-    };
-    auto weights = [&](const Item& t, int c, int s, const Sizes& z) {
-      uint8_t* p = ring + s * S::kSlot;
-      const size_t sf = (static_cast<size_t>(t.w_row >> 7) * a.wkb + c * S::kTiles) * 512;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(full + s, z.bytes);
-        tma_load_2d(p, &wmap, c * (kChunk / 2), t.w_row, full + s);
-        bulk_g2s(p + S::kSfOff, a.wsf + sf, z.tiles * 512, full + s);
-        if constexpr (MODE == kGated) {
-          tma_load_2d(p + kWBytes, &wmap2, c * (kChunk / 2), t.w_row, full + s);
-          bulk_g2s(p + S::kSfOff + S::kSf, a.wsf2 + sf, z.tiles * 512, full + s);
-        }
-      }
-    };
-    auto tokens = [&](const Item& t, int c, int s, const Sizes& z) {
-      uint8_t* p = ring + s * S::kSlot;
-      const uint8_t* sf = a.asf + (static_cast<size_t>(t.n0 >> 7) * a.wkb + c * S::kTiles) * 512;
-      const size_t next = static_cast<size_t>(a.wkb) * 512;
-      if (elect_one()) {
-        if constexpr (GROUPED) {
-          for (int r = 0; r < z.a_rows; r += 16) {
-            tma_load_2d(p + S::kW * kWBytes + r * 128, &amap, c * (kChunk / 2), t.n0 + r, full + s);
-          }
-        } else {
-          tma_load_2d(p + S::kW * kWBytes, &amap, c * (kChunk / 2), t.n0, full + s);
-        }
-        bulk_g2s(p + S::kSfOff + S::kW * S::kSf, sf, z.tiles * 512, full + s);
-        if (S::kRowTiles > 1 && z.row_tiles > 1) {
-          bulk_g2s(p + S::kSfOff + (S::kW + 1) * S::kSf, sf + next, z.tiles * 512, full + s);
-        }
-      }
-    };
-    static_assert(S::kRowTiles <= 2, "token scale tiles");
-    // With early weights the first ring of weight copies goes out before the
-    // wait for the preceding kernel, the token copies of those slots after it.
-    int ahead = 0;
-    if constexpr (!GROUPED) {
-      Walk<NT, GROUPED> w2 = w;
-      if (a.early != 0) {
-        while (ahead < ST && w2.next(a, it)) {
-          for (int c = it.c0; c < it.c1 && ahead < ST; ++c, ++ahead) weights(it, c, ahead, sizes(it, c));
-        }
-      }
-      pdl_wait();
-      // After the wait, so that whatever precedes this kernel is complete when
-      // the next one starts.
-      pdl_launch_dependents();
-    }
-    int n = 0;  // chunks so far
+    int slot = 0, turn = 0, n = 0;
     while (ok && w.next(a, it)) {
       for (int c = it.c0; c < it.c1; ++c) {
         if (n >= ST && !warp_wait(empty + slot, turn ^ 1)) {
           ok = false;
           break;
         }
-        const Sizes z = sizes(it, c);
-        if (n >= ahead) weights(it, c, slot, z);
-        if constexpr (!FUSED) tokens(it, c, slot, z);
+        const int bytes = min(S::kTiles, a.wkb - c * S::kTiles) * 512;
+        uint8_t* p = ring + slot * S::kSlot;
+        const size_t sf = (static_cast<size_t>(it.w_row >> 7) * a.wkb + c * S::kTiles) * 512;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full + slot, S::kW * (kWBytes + bytes));
+          tma_load_2d(p, &wmap, c * (kChunk / 2), it.w_row, full + slot);
+          bulk_g2s(p + S::kSfOff, a.wsf + sf, bytes, full + slot);
+          if constexpr (MODE == kGated) {
+            tma_load_2d(p + kWBytes, &wmap2, c * (kChunk / 2), it.w_row, full + slot);
+            bulk_g2s(p + S::kSfOff + S::kSf, a.wsf2 + sf, bytes, full + slot);
+          }
+        }
+        ++n;
+        if (++slot == ST) {
+          slot = 0;
+          turn ^= 1;
+        }
+      }
+    }
+  } else if (!FUSED && warp == 2) {
+    if constexpr (!GROUPED) {
+      pdl_wait();
+      // After the wait, so that whatever precedes this kernel is complete when
+      // the next one starts.
+      pdl_launch_dependents();
+    }
+    static_assert(S::kRowTiles <= 2, "token scale tiles");
+    Walk<NT, GROUPED> w(a, first);
+    Item it;
+    int slot = 0, turn = 0, n = 0;
+    while (ok && w.next(a, it)) {
+      const int row_tiles = min(S::kRowTiles, a.a_row_tiles - (it.n0 >> 7));
+      const int boxes = (min(it.n_valid, NT) + S::kBox - 1) / S::kBox;
+      for (int c = it.c0; c < it.c1; ++c) {
+        if (n >= ST && !warp_wait(empty + slot, turn ^ 1)) {
+          ok = false;
+          break;
+        }
+        const int bytes = min(S::kTiles, a.wkb - c * S::kTiles) * 512;
+        uint8_t* p = ring + slot * S::kSlot + S::kW * kWBytes;
+        uint8_t* psf = ring + slot * S::kSlot + S::kSfOff + S::kW * S::kSf;
+        const uint8_t* sf = a.asf + (static_cast<size_t>(it.n0 >> 7) * a.wkb + c * S::kTiles) * 512;
+        const size_t next = static_cast<size_t>(a.wkb) * 512;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full + slot, boxes * S::kBox * 128 + row_tiles * bytes);
+          for (int i = 0; i < boxes; ++i) {
+            tma_load_2d(p + i * S::kBox * 128, &amap, c * (kChunk / 2), it.n0 + i * S::kBox, full + slot);
+          }
+          bulk_g2s(psf, sf, bytes, full + slot);
+          if (S::kRowTiles > 1 && row_tiles > 1) bulk_g2s(psf + S::kSf, sf + next, bytes, full + slot);
+        }
         ++n;
         if (++slot == ST) {
           slot = 0;
@@ -588,7 +581,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         constexpr int kPer = FMT == HQ_FP4_NV ? 1 : 2;  // threads per block
         tok_sf[c * kTokenScales<FMT> + blk / (4 * kPer) * 128 + t.row * 16 + (blk / kPer & 3)] = static_cast<uint8_t>(q.byte);
       };
-      At t0{0, static_cast<int>(threadIdx.x) - 64 - kWorkers}, t1;
+      At t0{0, static_cast<int>(threadIdx.x) - 32 * S::kRoles - kWorkers}, t1;
       float v0[16], v1[16];
       step(t0);
       load_token(a, t0.row, t0.b * 16, v0);
@@ -606,8 +599,8 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(tok_full);
     }
-    if (warp >= 2 + S::kTokWarps) {
-    const int ew = warp - 2 - S::kTokWarps, quarter = warp & 3;
+    if (warp >= S::kRoles + S::kTokWarps) {
+    const int ew = warp - S::kRoles - S::kTokWarps, quarter = warp & 3;
     constexpr int kParts = S::kEpiWarps / 4;  // warps that share a lane quarter split the columns
     const int col0 = (ew >> 2) * (NT / kParts), col1 = col0 + NT / kParts;
     const int mrow = quarter * 32 + lane;
@@ -1005,6 +998,7 @@ cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, c
   e = launch_quantize(l.fmt, xd, x, ldx, l.T, l.H, x_scale, ws + o.xc, ws + o.xs, nullptr, pos, l.k, rows, st);
   if (e != cudaSuccess) return e;
   const int nt = static_cast<long>(l.T) * l.k > 48l * l.E ? 128 : 64;
+  const int box = nt == 128 ? Shape<HQ_FP4_NV, 128, kGated>::kBox : Shape<HQ_FP4_NV, 64, kGated>::kBox;
   const int grid = std::min(sm_count(), kMaxGrid);
   CUtensorMap wmap, wmap2, amap;
   GemmArgs a{};
@@ -1016,7 +1010,7 @@ cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, c
 
   if ((e = code_map(&wmap, gate->codes, gate->rows, l.H, kM)) != cudaSuccess) return e;
   if ((e = code_map(&wmap2, up->codes, up->rows, l.H, kM)) != cudaSuccess) return e;
-  if ((e = code_map(&amap, ws + o.xc, l.rows, l.H, 16)) != cudaSuccess) return e;
+  if ((e = code_map(&amap, ws + o.xc, l.rows, l.H, box)) != cudaSuccess) return e;
   a.wsf = gate->scales;
   a.wts = gate->tensor_scale;
   a.n_wts = gate->n_tensor_scales;
@@ -1039,7 +1033,7 @@ cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, c
   if (e != cudaSuccess) return e;
 
   if ((e = code_map(&wmap, down->codes, down->rows, l.I, kM)) != cudaSuccess) return e;
-  if ((e = code_map(&amap, ws + o.hc, l.rows, l.I, 16)) != cudaSuccess) return e;
+  if ((e = code_map(&amap, ws + o.hc, l.rows, l.I, box)) != cudaSuccess) return e;
   a.wsf = down->scales;
   a.wts = down->tensor_scale;
   a.n_wts = down->n_tensor_scales;
