@@ -181,7 +181,7 @@ struct GemmArgs {
   uint8_t* h_codes;
   uint8_t* h_scales;
   int h_kb;
-  int early;           // the weights may be read before the preceding kernel ends
+  int early;           // the weights (grouped: and the segments) may be read before the preceding kernel ends
   // fused: the tokens
   const void* x;
   int x_dtype;
@@ -414,15 +414,11 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   tc::tc_fence_after();
   const uint32_t tmem = *tslot;
   const uint32_t sf_cols = tmem + S::kAccs * S::kW * NT;
-  if constexpr (GROUPED) {
-    pdl_wait();  // the segments come from the sort
-    pdl_launch_dependents();
-    load_groups<NT>(a, first);
-  }
+  if constexpr (GROUPED) load_groups<NT>(a, first);
   bool ok = true;
 
   if (warp == 0) {
-    if (!GROUPED && a.early == 0) pdl_wait();
+    if (a.early == 0) pdl_wait();
     if (FUSED) pdl_launch_dependents();
     Walk<NT, GROUPED> w(a, first);
     Item it;
@@ -453,12 +449,10 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       }
     }
   } else if (!FUSED && warp == 2) {
-    if constexpr (!GROUPED) {
-      pdl_wait();
-      // After the wait, so that whatever precedes this kernel is complete when
-      // the next one starts.
-      pdl_launch_dependents();
-    }
+    pdl_wait();
+    // After the wait, so that whatever precedes this kernel is complete when
+    // the next one starts.
+    pdl_launch_dependents();
     static_assert(S::kRowTiles <= 2, "token scale tiles");
     Walk<NT, GROUPED> w(a, first);
     Item it;
@@ -555,7 +549,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       acc = accn % S::kAccs;
     }
   } else {
-    if constexpr (!GROUPED) pdl_wait();
+    pdl_wait();
     if constexpr (FUSED) {
       // All of the tokens, once per CTA, while the first weights are on their
       // way: a thread takes 16 values, two loads ahead of each other.
@@ -1002,6 +996,9 @@ cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, c
   const int grid = std::min(sm_count(), kMaxGrid);
   CUtensorMap wmap, wmap2, amap;
   GemmArgs a{};
+  // Both products start behind a kernel that lets them start only after its own
+  // wait: by then the sort is complete, and so is all that came before the call.
+  a.early = 1;
   a.status = reinterpret_cast<uint32_t*>(ws);
   a.offsets = offsets;
   a.counts = counts;
