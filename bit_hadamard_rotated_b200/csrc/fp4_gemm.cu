@@ -26,10 +26,9 @@
 // Two accumulators where they fit (up to 128 tokens), so the next tile's MMAs
 // run under the epilogue.
 //
-// Few tiles: the (tile, chunk) units are split evenly over the CTAs, so a tile
-// may be shared by several; each leaves its partial sums in the workspace and
-// the last to arrive adds them in CTA order (the result does not depend on
-// who is last).
+// Few tiles of a long K: several CTAs take a part of a tile's K each and leave
+// their sums in the workspace; the last to arrive adds them in the order of the
+// parts (the result does not depend on who is last).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -131,12 +130,11 @@ struct Shape {
   static constexpr int kW = MODE == kGated ? 2 : 1;                      // weight tiles per slot
   static constexpr int kTiles = kChunk / (FMT == HQ_FP4_NV ? 64 : 128);  // scale tiles per chunk
   static constexpr int kSf = kTiles * 512;                               // one row tile's scales
-  static constexpr int kRowTiles = NT > 128 ? NT / 128 : 1;              // token scale tiles
   static constexpr int kABytes = MODE == kFused ? 0 : NT * kChunk / 2;
   static constexpr int kSfOff = kW * kWBytes + kABytes;                  // scales: weights', then tokens'
-  static constexpr int kSlot = kSfOff + (MODE == kFused ? kW : kW + kRowTiles) * kSf;
+  static constexpr int kSlot = kSfOff + (MODE == kFused ? kW : kW + 1) * kSf;
   static constexpr int kAccs = kW * NT <= 128 ? 2 : 1;                   // accumulator sets
-  static constexpr int kSfCols = kTiles * 4 * (kW + kRowTiles);          // one slot's scales
+  static constexpr int kSfCols = kTiles * 4 * (kW + 1);                  // one slot's scales
   static constexpr bool kGroups = MODE == kGrouped || MODE == kGated;
   static constexpr int kTokWarps = MODE == kFused ? 4 : 0;               // quantise tokens beside the epilogue's
   static constexpr int kEpiWarps = MODE == kFused ? 4 : MODE == kGated && NT > 64 ? 16 : 8;
@@ -162,13 +160,13 @@ struct GemmArgs {
   int M, N, C;         // weight rows (of one expert), tokens, chunks of K
   int k_steps;         // MMAs of 64 over the whole of K
   int mt, nt;          // tiles
-  int units;           // split: mt * nt * C (whole tiles: 0)
+  int split;           // parts of a tile's K, each a CTA's (1: whole tiles)
   void* y;
   int y_dtype;
   size_t ldy;
   uint32_t* status;
-  uint32_t* counters;  // split: per CTA, zero between calls
-  float* part;         // split: 2 slots of [NT][128] per CTA
+  uint32_t* counters;  // split: arrivals per tile and epilogue warp, zero between calls
+  float* part;         // split: [NT][128] sums per CTA
   // grouped: the experts' row segments; tiles are (expert, token tile, m tile)
   const int32_t* offsets;
   const int32_t* counts;
@@ -234,12 +232,9 @@ struct Walk {
       const int t = u - uniform(first[e]);
       ni = t / a.mt;
       mi = t - ni * a.mt;
-    } else if (a.units == 0) {
-      u = blockIdx.x;
-      end = a.mt * a.nt;
     } else {
-      u = static_cast<int>(static_cast<long>(a.units) * blockIdx.x / gridDim.x);
-      end = static_cast<int>(static_cast<long>(a.units) * (blockIdx.x + 1) / gridDim.x);
+      u = blockIdx.x / a.split;
+      end = a.mt * a.nt;
     }
   }
   // The next item; false at the end.
@@ -266,14 +261,12 @@ struct Walk {
       ++mi;
       ++u;
     } else {
-      int tile = u;
-      if (a.units > 0) {
-        tile = u / a.C;
-        it.c0 = u - tile * a.C;
-        it.c1 = min(a.C, it.c0 + end - u);
-        u += it.c1 - it.c0;
-      } else {
-        u += gridDim.x;
+      const int tile = u;
+      u += gridDim.x;  // parts: one per CTA
+      if (a.split > 1) {
+        const int part = blockIdx.x - tile * a.split;
+        it.c0 = a.C * part / a.split;
+        it.c1 = a.C * (part + 1) / a.split;
       }
       // token tiles fastest: CTAs that run together share weight tiles in L2
       const int mi_ = tile / a.nt, ni_ = tile - mi_ * a.nt;
@@ -453,12 +446,10 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     // After the wait, so that whatever precedes this kernel is complete when
     // the next one starts.
     pdl_launch_dependents();
-    static_assert(S::kRowTiles <= 2, "token scale tiles");
     Walk<NT, GROUPED> w(a, first);
     Item it;
     int slot = 0, turn = 0, n = 0;
     while (ok && w.next(a, it)) {
-      const int row_tiles = min(S::kRowTiles, a.a_row_tiles - (it.n0 >> 7));
       const int boxes = (min(it.n_valid, NT) + S::kBox - 1) / S::kBox;
       for (int c = it.c0; c < it.c1; ++c) {
         if (n >= ST && !warp_wait(empty + slot, turn ^ 1)) {
@@ -469,14 +460,12 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         uint8_t* p = ring + slot * S::kSlot + S::kW * kWBytes;
         uint8_t* psf = ring + slot * S::kSlot + S::kSfOff + S::kW * S::kSf;
         const uint8_t* sf = a.asf + (static_cast<size_t>(it.n0 >> 7) * a.wkb + c * S::kTiles) * 512;
-        const size_t next = static_cast<size_t>(a.wkb) * 512;
         if (elect_one()) {
-          mbar_arrive_expect_tx(full + slot, boxes * S::kBox * 128 + row_tiles * bytes);
+          mbar_arrive_expect_tx(full + slot, boxes * S::kBox * 128 + bytes);
           for (int i = 0; i < boxes; ++i) {
             tma_load_2d(p + i * S::kBox * 128, &amap, c * (kChunk / 2), it.n0 + i * S::kBox, full + slot);
           }
           bulk_g2s(psf, sf, bytes, full + slot);
-          if (S::kRowTiles > 1 && row_tiles > 1) bulk_g2s(psf + S::kSf, sf + next, bytes, full + slot);
         }
         ++n;
         if (++slot == ST) {
@@ -520,10 +509,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
           for (int t = 0; t < S::kTiles; ++t) {
 #pragma unroll
             for (int i = 0; i < S::kW; ++i) tc_copy_scales(sfa + 4 * (i * S::kTiles + t), sp + i * S::kSf + 512 * t);
-#pragma unroll
-            for (int r = 0; r < S::kRowTiles; ++r) {
-              tc_copy_scales(sfb + 4 * (t * S::kRowTiles + r), sp_tok + S::kSf * r + (FUSED ? 128 : 512) * t);
-            }
+            tc_copy_scales(sfb + 4 * t, sp_tok + (FUSED ? 128 : 512) * t);
           }
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
@@ -532,7 +518,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
               for (int i = 0; i < S::kW; ++i) {
                 const int t = FMT == HQ_FP4_NV ? s : s >> 1, id = FMT == HQ_FP4_NV ? 0 : 2 * (s & 1);
                 tc_mma_scaled<FMT>(d + i * NT, da + i * (kWBytes >> 4) + 2 * s, db + 2 * s, idesc_fp4(FMT, n_mma, id),
-                                   sfa + 4 * (i * S::kTiles + t), sfb + 4 * t * S::kRowTiles + half,
+                                   sfa + 4 * (i * S::kTiles + t), sfb + 4 * t + half,
                                    s > 0 ? 1u : first_sum);
               }
             }
@@ -678,14 +664,9 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(dempty + acc);
       } else if constexpr (!GROUPED) {
-        // a tile shared by CTAs i0 .. i1: the units [t C, t C + C)
-        const int t = (it.m0 / kM) * a.nt + it.n0 / NT;
-        const long u0 = static_cast<long>(t) * a.C, u1 = u0 + a.C - 1;
-        const int i0 = static_cast<int>(((u0 + 1) * gridDim.x - 1) / a.units);
-        const int i1 = static_cast<int>(((u1 + 1) * gridDim.x - 1) / a.units);
-        const size_t part_size = static_cast<size_t>(NT) * kM;
-        // a CTA's second slot is for the tile that it begins
-        float* mine = a.part + (2 * static_cast<size_t>(blockIdx.x) + (it.c0 == 0 ? 1 : 0)) * part_size;
+        const int tile = blockIdx.x / a.split;
+        constexpr size_t kPart = static_cast<size_t>(NT) * kM;
+        float* mine = a.part + blockIdx.x * kPart;
         for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
           float f[16];
           load_columns<16>(d + c, f);
@@ -696,12 +677,12 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(dempty + acc);
         // Each warp's share of the tile is counted on its own: the last of the
-        // tile's CTAs to bring it adds the parts.
+        // tile's CTAs to bring it adds the parts, in their order.
         uint32_t last = 0;
-        uint32_t* counter = a.counters + i0 * kMaxEpiWarps + ew;
+        uint32_t* counter = a.counters + tile * kMaxEpiWarps + ew;
         if (lane == 0 && col0 < it.n_valid) {
           __threadfence();
-          last = atomicAdd(counter, 1u) == static_cast<uint32_t>(i1 - i0) ? 1u : 0u;
+          last = atomicAdd(counter, 1u) == static_cast<uint32_t>(a.split - 1) ? 1u : 0u;
         }
         if (__shfl_sync(~0u, last, 0) != 0) {
           __threadfence();
@@ -710,8 +691,8 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
             float f[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) f[j] = 0.f;
-            for (int i = i0; i <= i1; ++i) {  // 16 loads in flight
-              const float* p = a.part + (2 * static_cast<size_t>(i) + (i == i0 ? 1 : 0)) * part_size + c * kM + mrow;
+            for (int i = 0; i < a.split; ++i) {  // 16 loads in flight
+              const float* p = a.part + (static_cast<size_t>(tile) * a.split + i) * kPart + c * kM + mrow;
               float v[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) v[j] = __ldcg(p + j * kM);
@@ -738,6 +719,287 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   if (warp == 1) tc::tmem_dealloc(tmem, S::kCols);
 }
 
+// ------------------------------------------------------------------ pairs
+//
+// Large products: two CTAs of a cluster on one tile of 256 weight rows x 256
+// tokens (cta_group::2).  Each brings its own 128 weight rows and half of the
+// tokens, and the tensor cores of both read both halves, so a chunk costs each
+// SM 36 KB of copies and 32 KB of operand reads instead of 54 and 48: a single
+// CTA's 128 x 256 tile is bound by shared-memory bandwidth (about 108 KB a
+// chunk, 843 cycles at 128 bytes a cycle, for 512 cycles of MMAs).
+//
+// The even CTA's MMA warp issues for both.  It waits for its own slot and for
+// the odd CTA's, whose warp 1 passes its slots' arrivals on; commits free the
+// slots and hand over the accumulators in both CTAs.
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrive on CTA 0's barrier at the address of this CTA's `bar`.  What the
+// arrivals pass on is not plain memory (copies that have landed, accumulators
+// that have been read: tcgen05 fences order those), so neither side fences at
+// cluster scope; a fence per chunk took the 512-cycle chunk to 2500.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+}
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void pair_copy_scales(uint32_t taddr, uint32_t smem) {
+  const uint64_t desc = tc::smem_desc(smem, 0, 128);
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+template <int FMT>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                         uint32_t accumulate) {
+  if constexpr (FMT == HQ_FP4_NV) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  }
+}
+
+template <int FMT>
+struct PairShape {
+  static constexpr int NT = 256;
+  static constexpr int kTiles = kChunk / (FMT == HQ_FP4_NV ? 64 : 128);
+  static constexpr int kSf = kTiles * 512;
+  static constexpr int kABytes = NT / 2 * kChunk / 2;
+  static constexpr int kSfOff = kWBytes + kABytes;
+  static constexpr int kSlot = (kSfOff + 3 * kSf + 1023) / 1024 * 1024;
+  static constexpr int kStages = (kSmemMax - 2048) / kSlot;
+  static constexpr int kSfCols = kTiles * 4 * 3;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = 32 * (3 + kEpiWarps);
+  static_assert(NT + 2 * kSfCols <= 512, "tensor memory");
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(PairShape<FMT>::kThreads, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap, const GemmArgs a) {
+  using S = PairShape<FMT>;
+  constexpr int NT = S::NT, ST = S::kStages;
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + ST * S::kSlot);
+  uint64_t* peer = full + ST;  // CTA 0: the other CTA's slot is full
+  uint64_t* empty = peer + ST;
+  uint64_t* dfull = empty + ST;
+  uint64_t* dempty = dfull + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(dempty + 1);
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int rank = uniform(static_cast<int>(cluster_rank()));
+  const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1, tiles = a.mt * a.nt;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(full + i, 2);
+      mbar_init(peer + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    mbar_init(dfull, 1);
+    mbar_init(dempty, 2 * S::kEpiWarps);
+    fence_mbar_init();
+    prefetch_tensormap(&wmap);
+    prefetch_tensormap(&amap);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tslot, sf_cols = tmem + NT;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (a.early == 0) pdl_wait();
+    int slot = 0, turn = 0, n = 0;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const int row = t / a.nt * 256 + rank * kM;
+      for (int c = 0; c < a.C; ++c) {
+        if (n >= ST && !warp_wait(empty + slot, turn ^ 1)) {
+          ok = false;
+          break;
+        }
+        // an odd number of row tiles: the last pair's second CTA has no weights
+        // (its copies read zeros past the last row) and no scales
+        const int bytes = row < a.M ? min(S::kTiles, a.wkb - c * S::kTiles) * 512 : 0;
+        uint8_t* p = ring + slot * S::kSlot;
+        const uint8_t* sf = a.wsf + (static_cast<size_t>(row >> 7) * a.wkb + c * S::kTiles) * 512;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full + slot, kWBytes + bytes);
+          tma_load_2d(p, &wmap, c * (kChunk / 2), row, full + slot);
+          if (bytes > 0) bulk_g2s(p + S::kSfOff, sf, bytes, full + slot);
+        }
+        ++n;
+        if (++slot == ST) {
+          slot = 0;
+          turn ^= 1;
+        }
+      }
+    }
+  } else if (warp == 2) {
+    pdl_wait();
+    pdl_launch_dependents();  // after the wait, as in gemm_kernel
+    int slot = 0, turn = 0, n = 0;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const int n0 = t % a.nt * NT;
+      const int row_tiles = min(2, a.a_row_tiles - (n0 >> 7));
+      for (int c = 0; c < a.C; ++c) {
+        if (n >= ST && !warp_wait(empty + slot, turn ^ 1)) {
+          ok = false;
+          break;
+        }
+        const int bytes = min(S::kTiles, a.wkb - c * S::kTiles) * 512;
+        uint8_t* p = ring + slot * S::kSlot;
+        const uint8_t* sf = a.asf + (static_cast<size_t>(n0 >> 7) * a.wkb + c * S::kTiles) * 512;
+        const size_t next = static_cast<size_t>(a.wkb) * 512;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full + slot, S::kABytes + row_tiles * bytes);
+          tma_load_2d(p + kWBytes, &amap, c * (kChunk / 2), n0 + rank * (NT / 2), full + slot);
+          bulk_g2s(p + S::kSfOff + S::kSf, sf, bytes, full + slot);
+          if (row_tiles > 1) bulk_g2s(p + S::kSfOff + 2 * S::kSf, sf + next, bytes, full + slot);
+        }
+        ++n;
+        if (++slot == ST) {
+          slot = 0;
+          turn ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1 && rank != 0) {
+    int slot = 0, par = 0;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      for (int c = 0; c < a.C; ++c) {
+        if (!warp_wait(full + slot, par)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) arrive_leader(peer + slot);
+        if (++slot == ST) {
+          slot = 0;
+          par ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    const uint32_t d = uniform(tmem), sf0 = uniform(sf_cols), ring0 = uniform(smem_u32(ring));
+    int slot = 0, par = 0, n = 0, tile = 0;
+    // M = 256
+    constexpr uint32_t kIdesc = idesc_fp4(FMT, NT, 0) - (static_cast<uint32_t>(kM >> 4) << 24) + (16u << 24);
+    for (int t = pair; ok && t < tiles; t += pairs, ++tile) {
+      if (tile > 0 && !warp_wait(dempty, (tile - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      for (int c = 0; c < a.C; ++c) {
+        if (!warp_wait(full + slot, par) || !warp_wait(peer + slot, par)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t p = ring0 + slot * S::kSlot;
+        const uint32_t sfa = sf0 + (n & 1) * S::kSfCols, sfb = sfa + S::kTiles * 4, sp = p + S::kSfOff;
+        const uint64_t da = desc_sw128(p), db = desc_sw128(p + kWBytes);
+        const int steps = min(4, a.k_steps - 4 * c);
+        const uint32_t first_sum = c > 0 ? 1u : 0u;
+        ++n;
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < S::kTiles; ++i) {
+            pair_copy_scales(sfa + 4 * i, sp + 512 * i);
+            pair_copy_scales(sfb + 8 * i, sp + S::kSf + 512 * i);
+            pair_copy_scales(sfb + 8 * i + 4, sp + 2 * S::kSf + 512 * i);
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            if (s < steps) {
+              const int i = FMT == HQ_FP4_NV ? s : s >> 1;
+              const uint32_t id = FMT == HQ_FP4_NV ? 0u : 2u * (s & 1);
+              pair_mma<FMT>(d, da + 2 * s, db + 2 * s, kIdesc | id << 29 | id << 4, sfa + 4 * i, sfb + 8 * i,
+                            s > 0 ? 1u : first_sum);
+            }
+          }
+          pair_commit(empty + slot);
+          if (c + 1 == a.C) pair_commit(dfull);
+        }
+        if (++slot == ST) {
+          slot = 0;
+          par ^= 1;
+        }
+      }
+    }
+  } else {
+    pdl_wait();
+    const int ew = warp - 3, quarter = warp & 3;
+    const int col0 = (ew >> 2) * (NT / 2), col1 = col0 + NT / 2;
+    const int mrow = quarter * 32 + lane;
+    const float alpha = (a.wts != nullptr ? __ldg(a.wts) : 1.f) * (a.ats != nullptr ? __ldg(a.ats) : 1.f);
+    const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    int tile = 0;
+    for (int t = pair; ok && t < tiles; t += pairs, ++tile) {
+      if (!warp_wait(dfull, tile & 1)) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      const int n0 = t % a.nt * NT, n_valid = min(NT, a.N - n0);
+      const int m = t / a.nt * 256 + rank * kM + mrow;
+      for (int c = col0; c < col1 && c < n_valid; c += 32) {
+        float f[32];
+        load_columns<32>(d + c, f);
+        if (c + 32 >= min(col1, n_valid)) {  // the warp's last: the accumulators are read
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_leader(dempty);
+        }
+        if (m < a.M) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] *= alpha;
+          store_any<32>(a, n0 + c, m, f, n_valid - c);
+        }
+      }
+      if (col0 >= n_valid) {
+        __syncwarp();
+        if (lane == 0) arrive_leader(dempty);
+      }
+    }
+  }
+  if (!ok) record_error(a.status, HQ_DEV_TIMEOUT);
+  __syncwarp();
+  tc::tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no arrival or operand read of the other CTA is left
+  if (warp == 1) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
 // ------------------------------------------------------------------ host
 
 constexpr size_t kStatusBytes = 256;
@@ -746,37 +1008,55 @@ constexpr int kMaxGrid = static_cast<int>(kCounterBytes / 4 / kMaxEpiWarps);
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-// How a dense product runs: tokens per tile, CTAs, and the (tile, chunk)
-// units if they are split evenly (0: whole tiles).
+// How a dense product runs.
 struct Plan {
-  int nt_size, mt, nt, C, grid, units;
+  int nt_size;  // tokens per tile
+  bool pair;    // tiles of 256 x 256, two CTAs each
+  int mt, nt, C, grid, split;
 };
 
-int tokens_per_tile(int N) { return N <= 32 ? 32 : N <= 64 ? 64 : N <= 128 ? 128 : 256; }
-
-// Room for every plan of up to N tokens: a workspace for N serves all smaller
-// batches too.
-size_t part_bound(int N, int K) {
-  return K <= kChunk ? 0
-                     : static_cast<size_t>(std::min(sm_count(), kMaxGrid)) * 2 * tokens_per_tile(N) * kM * sizeof(float);
+// Parts of a tile's K are worth their exchange from about 8 chunks each on, for
+// more than 32 tokens from 16 and three parts.  2048 x 8192: 16 tokens 9.0 us
+// in 4 parts, 10.9 in 9, 11.9 whole; 128 tokens 14.2 us in 4 parts, 20 in 9,
+// 14.3 whole; 8192 x 8192: 64 tokens 16.4 us in 2 parts, 14.3 whole.  12288 x
+// 4096 at 16 (96 tiles of 148 CTAs): 8.9 us whole, 11.6 split evenly over all
+// CTAs.
+int parts_of(long tiles, long sms, int nt_size, int C) {
+  const long s = std::min<long>(sms / tiles, C / (nt_size <= 32 ? 8 : 16));
+  return static_cast<int>(s < (nt_size <= 32 ? 2 : 3) ? 1 : s);
 }
 
 Plan plan_of(int M, int N, int K) {
   Plan p{};
+  const long sms = std::min(sm_count(), kMaxGrid);
   p.C = (K + kChunk - 1) / kChunk;
   p.mt = (M + kM - 1) / kM;
-  p.nt_size = tokens_per_tile(N);
+  p.nt_size = N <= 32 ? 32 : N <= 64 ? 64 : 128;
   p.nt = (N + p.nt_size - 1) / p.nt_size;
-  const int sms = std::min(sm_count(), kMaxGrid);
   const long tiles = static_cast<long>(p.mt) * p.nt;
-  const long units = tiles * p.C;
-  if (tiles % sms != 0 && tiles < 4l * sms && p.C > 1) {
-    p.grid = static_cast<int>(std::min<long>(sms, std::max(tiles, units / 2)));
-    p.units = static_cast<int>(units);
-  } else {
-    p.grid = static_cast<int>(std::min<long>(sms, tiles));
+  // More than one wave of 128 x 128 tiles: pairs.  4100 x 4128 at 333 tokens
+  // (99 tiles) 12.1 us, in pairs 13.6; 12288 x 4096 at 200 (192 tiles) 15.5 us,
+  // in pairs 12.1; 8192 x 8192 at 4096 129 us with 128 x 256 tiles, in pairs 115.
+  if (N > 128 && tiles > sms) {
+    p.pair = true;
+    p.nt_size = 256;
+    p.mt = (M + 255) / 256;
+    p.nt = (N + 255) / 256;
+    p.grid = static_cast<int>(std::min(sms / 2, static_cast<long>(p.mt) * p.nt) * 2);
+    return p;
   }
+  p.split = parts_of(tiles, sms, p.nt_size, p.C);
+  p.grid = static_cast<int>(std::min(sms, tiles * p.split));
   return p;
+}
+
+// Room for every plan of up to N tokens: a workspace for N serves all smaller
+// batches too.
+size_t part_bound(int N, int K) {
+  const int nt = N <= 32 ? 32 : N <= 64 ? 64 : 128;
+  return (K + kChunk - 1) / kChunk < 16
+             ? 0
+             : static_cast<size_t>(std::min(sm_count(), kMaxGrid)) * nt * kM * sizeof(float);
 }
 
 template <int FMT, int NT, int MODE>
@@ -815,13 +1095,36 @@ cudaError_t fused_launch(const CUtensorMap& wmap, GemmArgs& a, int grid, cudaStr
 }
 
 template <int FMT>
+cudaError_t pair_launch(const CUtensorMap& wmap, const CUtensorMap& amap, const GemmArgs& a, int grid,
+                        cudaStream_t st) {
+  using S = PairShape<FMT>;
+  const size_t smem = 1024 + static_cast<size_t>(S::kStages) * S::kSlot + 512;
+  cudaError_t e = cudaFuncSetAttribute(pair_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {2, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, pair_kernel<FMT>, wmap, amap, a);
+}
+
+template <int FMT>
 cudaError_t dense_launch(int nt, const CUtensorMap& wmap, const CUtensorMap& amap, const GemmArgs& a, int grid,
                          cudaStream_t st) {
   switch (nt) {
     case 32: return gemm_launch<FMT, 32, kDense>(wmap, wmap, amap, a, grid, st);
     case 64: return gemm_launch<FMT, 64, kDense>(wmap, wmap, amap, a, grid, st);
-    case 128: return gemm_launch<FMT, 128, kDense>(wmap, wmap, amap, a, grid, st);
-    default: return gemm_launch<FMT, 256, kDense>(wmap, wmap, amap, a, grid, st);
+    default: return gemm_launch<FMT, 128, kDense>(wmap, wmap, amap, a, grid, st);
   }
 }
 
@@ -853,7 +1156,7 @@ GemmArgs dense_args(const hq_fp4_matrix* w, const Plan& p, int N, void* y, hq_dt
   a.k_steps = (w->K + 63) / 64;
   a.mt = p.mt;
   a.nt = p.nt;
-  a.units = p.units;
+  a.split = p.split;
   a.y = y;
   a.y_dtype = yd;
   a.ldy = ldy;
@@ -888,12 +1191,16 @@ cudaError_t launch_matmul(const hq_fp4_matrix* w, const uint8_t* codes, const ui
   CUtensorMap wmap, amap;
   cudaError_t e = code_map(&wmap, w->codes, w->rows, w->K, kM);
   if (e != cudaSuccess) return e;
-  e = code_map(&amap, codes, N, w->K, p.nt_size);
+  e = code_map(&amap, codes, N, w->K, p.pair ? p.nt_size / 2 : p.nt_size);
   if (e != cudaSuccess) return e;
   GemmArgs a = dense_args(w, p, N, y, yd, ldy, ws, part);
   a.asf = scales;
   a.ats = ats;
   a.early = early ? 1 : 0;
+  if (p.pair) {
+    return w->format == HQ_FP4_NV ? pair_launch<HQ_FP4_NV>(wmap, amap, a, p.grid, st)
+                                  : pair_launch<HQ_FP4_MX>(wmap, amap, a, p.grid, st);
+  }
   return w->format == HQ_FP4_NV ? dense_launch<HQ_FP4_NV>(p.nt_size, wmap, amap, a, p.grid, st)
                                 : dense_launch<HQ_FP4_MX>(p.nt_size, wmap, amap, a, p.grid, st);
 }

@@ -169,6 +169,8 @@ SHAPES = [  # M, K, N
     (128, 256, 16), (128, 256, 1), (1, 32, 1), (128, 64, 32), (128, 32, 8), (300, 96, 5), (128, 1024, 64), (384, 512, 33),
     (4100, 4128, 2), (640, 8192, 1), (128, 2048, 128), (257, 1056, 129), (512, 512, 256), (1000, 736, 333), (2304, 4096, 70),
     (129, 16384, 3), (256, 288, 1025), (20000, 256, 7),
+    (9473, 544, 400), (4000, 1312, 1025), (19200, 64, 300),  # tiles of two CTAs
+    (512, 8192, 100), (300, 6432, 40), (200, 3872, 20), (130, 32768, 1),  # parts of K
 ]
 
 
