@@ -17,16 +17,22 @@ class MoePlan:
     without one), offsets int32 [n_experts + 1], counts int32 [n_experts];
     n_rows: rows that hold every possible routing of these sizes."""
 
-    def __init__(self, pos, ends, n_experts, n_rows, align):
-        self.pos, self._ends, self.n_experts, self.n_rows, self.align = pos, ends, n_experts, n_rows, align
+    def __init__(self, buf, T, k, n_experts, ends, n_rows, align):
+        self._buf, self._ends = buf, ends  # pos at its start, offsets and counts from `ends` on
+        self.T, self.k, self.n_experts, self.n_rows, self.align = T, k, n_experts, n_rows, align
+        self.device, self._pos = buf.device, buf.data_ptr()
+
+    @property
+    def pos(self):
+        return self._buf[:self.T * self.k].view(self.T, self.k)
 
     @property
     def offsets(self):
-        return self._ends[:self.n_experts + 1]
+        return self._buf[self._ends:self._ends + self.n_experts + 1]
 
     @property
     def counts(self):
-        return self._ends[self.n_experts + 1:]
+        return self._buf[self._ends + self.n_experts + 1:self._ends + 2 * self.n_experts + 1]
 
 
 def hq_moe_sort(topk_ids: torch.Tensor, n_experts: int, align: int = 1, workspace: torch.Tensor | None = None,
@@ -42,16 +48,20 @@ def hq_moe_sort(topk_ids: torch.Tensor, n_experts: int, align: int = 1, workspac
 
 def _sort(ids, E, align, ws, stream):
     dev, (T, k) = ids.device, ids.shape
-    if ws is None:
-        ws = torch.empty(max(int(lib().hq_moe_sort_workspace_size(T, k, E)), 256), dtype=torch.uint8, device=dev)
-    pos = torch.empty_like(ids)
-    ends = torch.empty(max(2 * E + 1, 1), dtype=torch.int32, device=dev)
-    p = ends.data_ptr()
-    st = lib().hq_moe_sort(ids.data_ptr(), T, k, E, align, pos.data_ptr(), p, p + 4 * (E + 1), ws.data_ptr(), ws.numel(),
-                           _raw_stream(stream, dev.index))
+    L = lib()
+    need = int(L.hq_moe_sort_workspace_size(T, k, E))
+    # one allocation: pos, then offsets and counts, then the workspace, 256-byte aligned
+    ends = (T * k + 63) // 64 * 64
+    at = ends + (2 * max(E, 0) + 64) // 64 * 64
+    buf = torch.empty(at + (need // 4 if ws is None else 0), dtype=torch.int32, device=dev)
+    plan = MoePlan(buf, T, k, E, ends, T * k + min(E, T * k) * (align - 1), align)
+    p = plan._pos
+    wp, wn = (p + 4 * at, need) if ws is None else (ws.data_ptr(), ws.numel())
+    st = L.hq_moe_sort(ids.data_ptr(), T, k, E, align, p, p + 4 * ends, p + 4 * (ends + E + 1), wp, wn,
+                       _raw_stream(stream, dev.index))
     if st:
         check(st, "hq_moe_sort")
-    return MoePlan(pos, ends, E, T * k + min(E, T * k) * (align - 1), align)
+    return plan
 
 
 def _need_like(t, what, shape, dtype, dev):
@@ -61,14 +71,14 @@ def _need_like(t, what, shape, dtype, dev):
 
 def _need_rows(x, what, plan, tokens):
     """x [T][H] (tokens) or [n_rows][H], of a type the kernels take, on the plan's device."""
-    if x.dtype not in _DT or x.dim() != 2 or not x.is_contiguous() or x.device != plan.pos.device:
+    if x.dtype not in _DT or x.dim() != 2 or not x.is_contiguous() or x.device != plan.device:
         raise ValueError(f"{what} must be a contiguous fp16, bf16 or fp32 matrix on the plan's device")
-    if tokens and x.shape[0] != plan.pos.shape[0]:
-        raise ValueError(f"{what} must have one row per token, {plan.pos.shape[0]}")
+    if tokens and x.shape[0] != plan.T:
+        raise ValueError(f"{what} must have one row per token, {plan.T}")
 
 
 def _need_weights(topk_w, plan):
-    _need_like(topk_w, "topk_w", plan.pos.shape, torch.float32, plan.pos.device)
+    _need_like(topk_w, "topk_w", (plan.T, plan.k), torch.float32, plan.device)
 
 
 def hq_moe_gather(x: torch.Tensor, plan: MoePlan, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -84,8 +94,8 @@ def hq_moe_gather(x: torch.Tensor, plan: MoePlan, out: torch.Tensor | None = Non
 
 
 def _gather(x, plan, out, stream):
-    T, k = plan.pos.shape
-    st = lib().hq_moe_gather(x.data_ptr(), _DT[x.dtype], plan.pos.data_ptr(), T, k, x.shape[1], out.data_ptr(),
+    T, k = plan.T, plan.k
+    st = lib().hq_moe_gather(x.data_ptr(), _DT[x.dtype], plan._pos, T, k, x.shape[1], out.data_ptr(),
                              out.shape[0], _raw_stream(stream, x.device.index))
     if st:
         check(st, "hq_moe_gather")
@@ -94,8 +104,7 @@ def _gather(x, plan, out, stream):
 
 def _combine(rows, plan, topk_w, out_dtype, out, stream):
     _need_rows(rows, "rows", plan, False)
-    T, k = plan.pos.shape
-    H = rows.shape[1]
+    T, H = plan.T, rows.shape[1]
     dt = (rows.dtype if out is None else out.dtype) if out_dtype is None else out_dtype
     if dt not in _DT:
         raise ValueError("the output must be fp16, bf16 or fp32")
@@ -107,8 +116,8 @@ def _combine(rows, plan, topk_w, out_dtype, out, stream):
 
 
 def _launch_combine(rows, plan, topk_w, out, stream):
-    T, k = plan.pos.shape
-    st = lib().hq_moe_combine(rows.data_ptr(), _DT[rows.dtype], rows.shape[0], plan.pos.data_ptr(),
+    T, k = plan.T, plan.k
+    st = lib().hq_moe_combine(rows.data_ptr(), _DT[rows.dtype], rows.shape[0], plan._pos,
                               None if topk_w is None else topk_w.data_ptr(), T, k, rows.shape[1], out.data_ptr(),
                               _DT[out.dtype], _raw_stream(stream, rows.device.index))
     if st:
@@ -149,9 +158,9 @@ def hq_moe_combine_grad(dy: torch.Tensor, rows: torch.Tensor, plan: MoePlan, top
 
 
 def _combine_grad(dy, rows, plan, topk_w, out, stream):
-    T, k = plan.pos.shape
+    T, k = plan.T, plan.k
     dw = torch.empty_like(topk_w)
-    st = lib().hq_moe_combine_grad(dy.data_ptr(), _DT[dy.dtype], rows.data_ptr(), rows.shape[0], plan.pos.data_ptr(),
+    st = lib().hq_moe_combine_grad(dy.data_ptr(), _DT[dy.dtype], rows.data_ptr(), rows.shape[0], plan._pos,
                                    topk_w.data_ptr(), T, k, rows.shape[1], out.data_ptr(), dw.data_ptr(),
                                    _raw_stream(stream, dy.device.index))
     if st:
