@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from ._lib import HQ_FP4_MX, HQ_FP4_NV, HqFp4Matrix, check, lib
-from .hq import _DT, _need_cuda, _on_device, _ptr, _raw_stream
+from .hq import _DT, _need_cuda, _on, _ptr, _raw_stream
 
 _FMT = {"nv": HQ_FP4_NV, "mx": HQ_FP4_MX}
 
@@ -66,32 +66,36 @@ class Fp4Matrix:
         return self.c.K
 
 
-def _rows_in(x, K=None):
-    """x as rows the kernels read: 2-D, fp16/bf16/fp32, unit stride along K and
-    rows on 16-byte boundaries (copied if they are not)."""
+def _need_rows(x, K=None):
     if x.dtype not in _DT or x.dim() != 2 or (K is not None and x.shape[1] != K):
         raise ValueError(f"x must be fp16, bf16 or fp32 [rows][{'K' if K is None else K}]")
+
+
+def _rows_in(x):
+    """x as rows the kernels read: unit stride along K and rows on 16-byte
+    boundaries (copied if they are not), and its row stride."""
     if x.is_contiguous():
-        return x if x.data_ptr() % 16 == 0 else x.clone()
-    if x.stride(1) == 1 and x.stride(0) >= x.shape[1] and x.stride(0) * x.element_size() % 16 == 0 and x.data_ptr() % 16 == 0:
-        return x
-    return x.contiguous()
+        x = x if x.data_ptr() % 16 == 0 else x.clone()
+    elif x.stride(1) != 1 or x.stride(0) < x.shape[1] or x.stride(0) * x.element_size() % 16 or x.data_ptr() % 16:
+        x = x.contiguous()
+    return x, max(x.stride(0), x.shape[1])
 
 
 def hq_fp4_tensor_scale(x: torch.Tensor, stream=None) -> torch.Tensor:
     """max |x| / 2688 as an fp32 scalar tensor: the tensor scale that puts x's
     largest block at the end of the "nv" format's range (1 for zeros)."""
     _need_cuda(x)
-    x = _rows_in(x)
-    return _on_device(x.device, _tensor_scale, x, stream)
+    _need_rows(x)
+    return _on(x.device, stream, _tensor_scale, x)
 
 
-def _tensor_scale(x, stream):
+def _tensor_scale(x):
     dev = x.device
+    x, ldx = _rows_in(x)
     out = torch.empty((), dtype=torch.float32, device=dev)
     ws = torch.zeros(256, dtype=torch.uint8, device=dev)
-    check(lib().hq_fp4_tensor_scale(x.data_ptr(), _DT[x.dtype], max(x.stride(0), x.shape[1]), x.shape[0], x.shape[1],
-                                    out.data_ptr(), ws.data_ptr(), 256, _raw_stream(stream, dev.index)),
+    check(lib().hq_fp4_tensor_scale(x.data_ptr(), _DT[x.dtype], ldx, x.shape[0], x.shape[1],
+                                    out.data_ptr(), ws.data_ptr(), 256, _raw_stream(None, dev.index)),
           "hq_fp4_tensor_scale")
     return out
 
@@ -103,7 +107,7 @@ def hq_fp4_quantize(x: torch.Tensor, fmt: str = "nv", tensor_scale: torch.Tensor
     _need_cuda(x, tensor_scale)
     if fmt not in _FMT:
         raise ValueError('fmt must be "nv" or "mx"')
-    x = _rows_in(x)
+    _need_rows(x)
     if tensor_scale is not None:
         if fmt != "nv":
             raise ValueError('only "nv" takes a tensor scale')
@@ -111,11 +115,12 @@ def hq_fp4_quantize(x: torch.Tensor, fmt: str = "nv", tensor_scale: torch.Tensor
     if values is not True and values is not False and values is not None and (
             values.dtype != x.dtype or values.shape != x.shape or not values.is_contiguous() or values.device != x.device):
         raise ValueError("values must be a contiguous tensor of x's type and shape")
-    return _on_device(x.device, _quantize, x, fmt, tensor_scale, values, stream)
+    return _on(x.device, stream, _quantize, x, fmt, tensor_scale, values)
 
 
-def _quantize(x, fmt, tensor_scale, values, stream):
+def _quantize(x, fmt, tensor_scale, values):
     dev, (rows, K) = x.device, x.shape
+    x, ldx = _rows_in(x)
     if values is True:
         values = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif values is False:
@@ -124,8 +129,8 @@ def _quantize(x, fmt, tensor_scale, values, stream):
         torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
         torch.empty(_scale_shape(fmt, rows, K), dtype=torch.uint8, device=dev), fmt, tensor_scale, values)
     q.c.K = K  # as given: an odd K is refused below
-    st = lib().hq_fp4_quantize(x.data_ptr(), _DT[x.dtype], max(x.stride(0), K), q._ref,
-                               None if values is None else values.data_ptr(), _raw_stream(stream, dev.index))
+    st = lib().hq_fp4_quantize(x.data_ptr(), _DT[x.dtype], ldx, q._ref,
+                               None if values is None else values.data_ptr(), _raw_stream(None, dev.index))
     if st:
         check(st, "hq_fp4_quantize")
     return q
@@ -159,15 +164,15 @@ def hq_fp4_matmul(w: Fp4Matrix, a: Fp4Matrix, out_dtype: torch.dtype = torch.flo
     dev = w.codes.device
     if a.codes.device != dev:
         raise ValueError(f"a is on {a.codes.device}, the weights on {dev}")
-    return _on_device(dev, _matmul, w, a, out_dtype, out, workspace, stream)
+    return _on(dev, stream, _matmul, w, a, out_dtype, out, workspace)
 
 
-def _matmul(w, a, out_dtype, out, workspace, stream):
+def _matmul(w, a, out_dtype, out, workspace):
     dev = w.codes.device
     out, ldy = _out(out, a.rows, w.rows, out_dtype if out is None else out.dtype, dev)
     ws = _workspace(workspace, int(lib().hq_fp4_matmul_workspace_size(w._ref, a.rows)), dev)
     check(lib().hq_fp4_matmul(w._ref, a._ref, out.data_ptr(), _DT[out.dtype], ldy, ws.data_ptr(), ws.numel(),
-                              _raw_stream(stream, dev.index)), "hq_fp4_matmul")
+                              _raw_stream(None, dev.index)), "hq_fp4_matmul")
     return out
 
 
@@ -179,63 +184,90 @@ def hq_fp4_linear(w: Fp4Matrix, x: torch.Tensor, x_scale: torch.Tensor | None = 
     type unless out_dtype says otherwise."""
     _need_cuda(x, x_scale)
     dev = w.codes.device
-    x = _rows_in(x, w.K)
+    _need_rows(x, w.K)
     if x.device != dev:
         raise ValueError(f"x is on {x.device}, the weights on {dev}")
     _need_scale(x_scale, dev)
     dtype = out_dtype or (x.dtype if out is None else out.dtype)
-    return _on_device(dev, _linear, w, x, x_scale, dtype, out, workspace, stream)
+    return _on(dev, stream, _linear, w, x, x_scale, dtype, out, workspace)
 
 
-def _linear(w, x, x_scale, dtype, out, workspace, stream):
+def _linear(w, x, x_scale, dtype, out, workspace):
     dev, N = w.codes.device, x.shape[0]
+    x, ldx = _rows_in(x)
     out, ldy = _out(out, N, w.rows, dtype, dev)
     ws = workspace
     if ws is None or ws.device != dev or ws.dtype != torch.uint8:
         ws = _workspace(ws, int(lib().hq_fp4_linear_workspace_size(w._ref, N)), dev)
-    st = lib().hq_fp4_linear(w._ref, x.data_ptr(), _DT[x.dtype], max(x.stride(0), w.K), N,
+    st = lib().hq_fp4_linear(w._ref, x.data_ptr(), _DT[x.dtype], ldx, N,
                              None if x_scale is None else x_scale.data_ptr(), out.data_ptr(), _DT[dtype], ldy,
-                             ws.data_ptr(), ws.numel(), _raw_stream(stream, dev.index))
+                             ws.data_ptr(), ws.numel(), _raw_stream(None, dev.index))
     if st:
         check(st, "hq_fp4_linear")
     return out
 
 
-class Fp4Linear:
-    """A packed linear layer with its workspace: y = W q(x) (hq_fp4_linear).
-    x_scale: the activations' tensor scale ("nv"), or None.  One layer serves
-    one stream at a time."""
+class _Layer:
+    """A layer's workspace.  It grows with the calls; the ones it has outgrown
+    are kept, since a captured graph may still use them (each is at least twice
+    the one before)."""
 
-    def __init__(self, w: Fp4Matrix, x_scale: torch.Tensor | None = None, out_dtype: torch.dtype | None = None):
-        self.w, self.x_scale, self.out_dtype = w, x_scale, out_dtype
-        _need_scale(x_scale, w.codes.device)
-        self._ws, self._batch = None, 0
+    def __init__(self):
+        self._ws, self._outgrown = None, []
 
-    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-        w, dev = self.w, self.w.codes.device
-        if x.device != dev:
-            raise ValueError(f"x is on {x.device}, the weights on {dev}")
-        x = _rows_in(x, w.K)
-        N = x.shape[0]
-        if N > self._batch or self._ws is None:  # a workspace for N serves every smaller batch
-            self._ws, self._batch = _on_device(dev, _workspace, None, int(lib().hq_fp4_linear_workspace_size(w._ref, N)), dev), N
-        dtype = self.out_dtype or (x.dtype if out is None else out.dtype)
-        return _on_device(dev, _linear, w, x, self.x_scale, dtype, out, self._ws, stream)
+    def _grow(self, need, dev):
+        if self._ws is not None and need <= self._ws.numel():
+            return
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("call the layer once at this size before capturing it: its workspace has to grow")
+        if self._ws is not None:
+            self._outgrown.append(self._ws)
+            need = max(need, 2 * self._ws.numel())
+        self._ws = _workspace(None, need, dev)
 
     def check_status(self, stream=None):
+        """Raise HqError if a call on this layer recorded a device error."""
         if self._ws is not None:
             check(lib().hq_check_status(_ptr(self._ws), _raw_stream(stream, self._ws.device.index)), "device status")
 
 
-class Fp4Experts:
+class Fp4Linear(_Layer):
+    """A packed linear layer with its workspace: y = W q(x) (hq_fp4_linear).
+    x_scale: the activations' tensor scale ("nv"), or None.  One layer, captured
+    graphs of it included, serves one stream at a time."""
+
+    def __init__(self, w: Fp4Matrix, x_scale: torch.Tensor | None = None, out_dtype: torch.dtype | None = None):
+        super().__init__()
+        self.w, self.x_scale, self.out_dtype = w, x_scale, out_dtype
+        _need_scale(x_scale, w.codes.device)
+        self._batch = -1  # a workspace for a batch serves every smaller one
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        dev = self.w.codes.device
+        if x.device != dev:
+            raise ValueError(f"x is on {x.device}, the weights on {dev}")
+        _need_rows(x, self.w.K)
+        return _on(dev, stream, self._call, x, out)
+
+    def _call(self, x, out):
+        w, N = self.w, x.shape[0]
+        if N > self._batch:
+            self._grow(int(lib().hq_fp4_linear_workspace_size(w._ref, N)), w.codes.device)
+            self._batch = N
+        return _linear(w, x, self.x_scale, self.out_dtype or (x.dtype if out is None else out.dtype), out, self._ws)
+
+
+class Fp4Experts(_Layer):
     """The routed-expert layer on packed weights with its workspace
     (hq_fp4_experts): gate, up [n_experts * inter rows], down [n_experts *
     hidden rows].  x_scale, h_scale: tensor scales of the activations and of
-    h ("nv"), or None.  One layer serves one stream at a time."""
+    h ("nv"), or None.  One layer, captured graphs of it included, serves one
+    stream at a time."""
 
     def __init__(self, gate: Fp4Matrix, up: Fp4Matrix, down: Fp4Matrix, n_experts: int,
                  x_scale: torch.Tensor | None = None, h_scale: torch.Tensor | None = None,
                  out_dtype: torch.dtype | None = None):
+        super().__init__()
         dev = gate.codes.device
         if up.codes.device != dev or down.codes.device != dev:
             raise ValueError(f"the three matrices must be on one device, {dev}")
@@ -244,7 +276,7 @@ class Fp4Experts:
         self.gate, self.up, self.down, self.n_experts = gate, up, down, int(n_experts)
         self.x_scale, self.h_scale, self.out_dtype = x_scale, h_scale, out_dtype
         self.hidden = gate.K
-        self._ws, self._room = None, (0, 0, None)
+        self._room = (-1, 0, None)
         if not self._need(1, 1, torch.float32):
             raise ValueError("unsupported expert layer: formats, sizes or tensor scales do not fit together")
 
@@ -256,7 +288,7 @@ class Fp4Experts:
                  stream=None) -> torch.Tensor:
         """y [T][hidden] of x [T][hidden], topk_ids int32 [T][k], topk_w fp32 [T][k]."""
         dev = self.gate.codes.device
-        x = _rows_in(x, self.hidden)
+        _need_rows(x, self.hidden)
         T = x.shape[0]
         if topk_ids.dtype != torch.int32 or topk_w.dtype != torch.float32 or topk_ids.dim() != 2 \
                 or topk_ids.shape[0] != T or topk_w.shape != topk_ids.shape:
@@ -264,29 +296,29 @@ class Fp4Experts:
         for t in (x, topk_ids, topk_w):
             if t.device != dev:
                 raise ValueError(f"a tensor is on {t.device}, the weights on {dev}")
-        return _on_device(dev, self._call, x, topk_ids.contiguous(), topk_w.contiguous(), out, stream)
-
-    def _call(self, x, ids, w, out, stream):
-        dev, (T, k) = x.device, ids.shape
         dtype = self.out_dtype or (x.dtype if out is None else out.dtype)
+        if out is not None and (out.dtype != dtype or tuple(out.shape) != (T, self.hidden) or not out.is_contiguous()
+                                or out.device != dev):
+            raise ValueError(f"out must be contiguous {dtype} [{T}][{self.hidden}] on {dev}")
+        return _on(dev, stream, self._call, x, topk_ids, topk_w, dtype, out)
+
+    def _call(self, x, ids, w, dtype, out):
+        dev, (T, k) = x.device, ids.shape
+        x, ldx = _rows_in(x)
+        ids, w = ids.contiguous(), w.contiguous()
         if out is None:
             out = torch.empty((T, self.hidden), dtype=dtype, device=dev)
-        elif out.dtype != dtype or tuple(out.shape) != (T, self.hidden) or not out.is_contiguous() or out.device != dev:
-            raise ValueError(f"out must be contiguous {dtype} [{T}][{self.hidden}] on {dev}")
         room = self._room
-        if self._ws is None or T > room[0] or k != room[1] or dtype != room[2]:
-            self._ws, self._room = _workspace(None, self._need(T, k, dtype), dev), (T, k, dtype)
+        if T > room[0] or k != room[1] or dtype != room[2]:
+            self._grow(self._need(T, k, dtype), dev)
+            self._room = (T, k, dtype)
         st = lib().hq_fp4_experts(self.gate._ref, self.up._ref, self.down._ref, self.n_experts, x.data_ptr(),
-                                  _DT[x.dtype], max(x.stride(0), self.hidden), T, ids.data_ptr(), w.data_ptr(), k,
+                                  _DT[x.dtype], ldx, T, ids.data_ptr(), w.data_ptr(), k,
                                   _ptr(self.x_scale), _ptr(self.h_scale), out.data_ptr(), _DT[dtype],
-                                  self._ws.data_ptr(), self._ws.numel(), _raw_stream(stream, dev.index))
+                                  self._ws.data_ptr(), self._ws.numel(), _raw_stream(None, dev.index))
         if st:
             check(st, "hq_fp4_experts")
         return out
-
-    def check_status(self, stream=None):
-        if self._ws is not None:
-            check(lib().hq_check_status(_ptr(self._ws), _raw_stream(stream, self._ws.device.index)), "device status")
 
 
 __all__ = ["Fp4Experts", "Fp4Matrix", "Fp4Linear", "hq_fp4_tensor_scale", "hq_fp4_quantize", "hq_fp4_matmul", "hq_fp4_linear"]

@@ -33,8 +33,13 @@ def _raw_stream(stream, device_index):
     return get(device_index) if get is not None else torch.cuda.current_stream().cuda_stream
 
 
-def _on_device(dev, fn, *args):
-    """fn(*args) with dev as the current device (left alone where it already is)."""
+def _on(dev, stream, fn, *args):
+    """fn(*args) with dev as the current device and `stream`, where one is given,
+    as its current stream (so that what the call allocates, zeroes and copies
+    belongs to the stream that it runs on)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fn(*args)
     if dev.index == torch.cuda.current_device():
         return fn(*args)
     with torch.cuda.device(dev):

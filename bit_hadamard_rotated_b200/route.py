@@ -9,7 +9,7 @@ from __future__ import annotations
 import torch
 
 from ._lib import check, lib
-from .hq import _DT, _need_cuda, _on_device, _raw_stream
+from .hq import _DT, _need_cuda, _on, _raw_stream
 
 
 class MoePlan:
@@ -43,10 +43,10 @@ def hq_moe_sort(topk_ids: torch.Tensor, n_experts: int, align: int = 1, workspac
     _need_cuda(topk_ids, workspace)
     if topk_ids.dtype != torch.int32 or topk_ids.dim() != 2 or not topk_ids.is_contiguous():
         raise ValueError("topk_ids must be a contiguous int32 [T][k] tensor")
-    return _on_device(topk_ids.device, _sort, topk_ids, int(n_experts), int(align), workspace, stream)
+    return _on(topk_ids.device, stream, _sort, topk_ids, int(n_experts), int(align), workspace)
 
 
-def _sort(ids, E, align, ws, stream):
+def _sort(ids, E, align, ws):
     dev, (T, k) = ids.device, ids.shape
     L = lib()
     need = int(L.hq_moe_sort_workspace_size(T, k, E))
@@ -58,7 +58,7 @@ def _sort(ids, E, align, ws, stream):
     p = plan._pos
     wp, wn = (p + 4 * at, need) if ws is None else (ws.data_ptr(), ws.numel())
     st = L.hq_moe_sort(ids.data_ptr(), T, k, E, align, p, p + 4 * ends, p + 4 * (ends + E + 1), wp, wn,
-                       _raw_stream(stream, dev.index))
+                       _raw_stream(None, dev.index))
     if st:
         check(st, "hq_moe_sort")
     return plan
@@ -85,18 +85,17 @@ def hq_moe_gather(x: torch.Tensor, plan: MoePlan, out: torch.Tensor | None = Non
     """Each token's row x[t] to the rows of its pairs: [n_rows][H] (rows without
     a pair are left as they are in `out`; a new tensor's are not initialised)."""
     _need_rows(x, "x", plan, True)
-    H = x.shape[1]
-    if out is None:
-        out = torch.empty((plan.n_rows, H), dtype=x.dtype, device=x.device)
-    else:
-        _need_like(out, "out", (out.shape[0], H), x.dtype, x.device)
-    return _on_device(x.device, _gather, x, plan, out, stream)
+    if out is not None:
+        _need_like(out, "out", (out.shape[0], x.shape[1]), x.dtype, x.device)
+    return _on(x.device, stream, _gather, x, plan, out)
 
 
-def _gather(x, plan, out, stream):
+def _gather(x, plan, out):
     T, k = plan.T, plan.k
+    if out is None:
+        out = torch.empty((plan.n_rows, x.shape[1]), dtype=x.dtype, device=x.device)
     st = lib().hq_moe_gather(x.data_ptr(), _DT[x.dtype], plan._pos, T, k, x.shape[1], out.data_ptr(),
-                             out.shape[0], _raw_stream(stream, x.device.index))
+                             out.shape[0], _raw_stream(None, x.device.index))
     if st:
         check(st, "hq_moe_gather")
     return out
@@ -108,18 +107,18 @@ def _combine(rows, plan, topk_w, out_dtype, out, stream):
     dt = (rows.dtype if out is None else out.dtype) if out_dtype is None else out_dtype
     if dt not in _DT:
         raise ValueError("the output must be fp16, bf16 or fp32")
-    if out is None:
-        out = torch.empty((T, H), dtype=dt, device=rows.device)
-    else:
+    if out is not None:
         _need_like(out, "out", (T, H), dt, rows.device)
-    return _on_device(rows.device, _launch_combine, rows, plan, topk_w, out, stream)
+    return _on(rows.device, stream, _launch_combine, rows, plan, topk_w, dt, out)
 
 
-def _launch_combine(rows, plan, topk_w, out, stream):
+def _launch_combine(rows, plan, topk_w, dt, out):
     T, k = plan.T, plan.k
+    if out is None:
+        out = torch.empty((T, rows.shape[1]), dtype=dt, device=rows.device)
     st = lib().hq_moe_combine(rows.data_ptr(), _DT[rows.dtype], rows.shape[0], plan._pos,
                               None if topk_w is None else topk_w.data_ptr(), T, k, rows.shape[1], out.data_ptr(),
-                              _DT[out.dtype], _raw_stream(stream, rows.device.index))
+                              _DT[out.dtype], _raw_stream(None, rows.device.index))
     if st:
         check(st, "hq_moe_combine")
     return out
@@ -150,19 +149,19 @@ def hq_moe_combine_grad(dy: torch.Tensor, rows: torch.Tensor, plan: MoePlan, top
     _need_weights(topk_w, plan)
     if rows.dtype != dy.dtype or rows.shape[1] != dy.shape[1]:
         raise ValueError("dy and rows must have one type and width")
+    if out is not None:
+        _need_like(out, "out", rows.shape, rows.dtype, rows.device)
+    return _on(dy.device, stream, _combine_grad, dy, rows, plan, topk_w, out)
+
+
+def _combine_grad(dy, rows, plan, topk_w, out):
+    T, k = plan.T, plan.k
     if out is None:
         out = torch.empty_like(rows)
-    else:
-        _need_like(out, "out", rows.shape, rows.dtype, rows.device)
-    return _on_device(dy.device, _combine_grad, dy, rows, plan, topk_w, out, stream)
-
-
-def _combine_grad(dy, rows, plan, topk_w, out, stream):
-    T, k = plan.T, plan.k
     dw = torch.empty_like(topk_w)
     st = lib().hq_moe_combine_grad(dy.data_ptr(), _DT[dy.dtype], rows.data_ptr(), rows.shape[0], plan._pos,
                                    topk_w.data_ptr(), T, k, rows.shape[1], out.data_ptr(), dw.data_ptr(),
-                                   _raw_stream(stream, dy.device.index))
+                                   _raw_stream(None, dy.device.index))
     if st:
         check(st, "hq_moe_combine_grad")
     return out, dw

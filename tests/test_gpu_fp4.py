@@ -162,7 +162,6 @@ def check_product(y, W, A, K):
     assert np.all(np.isfinite(got))
     err = np.abs(got - want)
     assert np.all(err <= tol), f"worst err/tol {np.max(err / tol):.3g} at {np.unravel_index(np.argmax(err / tol), err.shape)}"
-    return np.linalg.norm(err) / np.linalg.norm(want)
 
 
 SHAPES = [  # M, K, N
@@ -272,6 +271,46 @@ def test_captured_and_replayed():
         x.copy_(rows(3, 2048, torch.bfloat16, 20 + s))
         g.replay()
         assert torch.equal(y, hq_fp4_linear(w, x))
+
+
+def test_captured_graph_outlives_a_larger_batch():
+    """A graph of a small batch, then larger eager batches of the same layer (its workspace grows), then the graph again."""
+    w = weight(1024, 8192, "nv", 12, True)
+    layer = Fp4Linear(w)
+    x = rows(3, 8192, torch.bfloat16, 13).cuda()
+    y = layer(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer(x, out=y)
+    want = hq_fp4_linear(w, x)
+    for n in (40, 100, 700):
+        big = rows(n, 8192, torch.bfloat16, n).cuda()
+        assert torch.equal(layer(big), hq_fp4_linear(w, big))
+        junk = [torch.full((1 << 20,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(8)]  # would take freed memory
+        y.zero_()
+        g.replay()
+        assert torch.equal(y, want)
+        del junk
+    with pytest.raises(RuntimeError):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            Fp4Linear(w)(x, out=y)
+    assert torch.equal(layer(x), want)
+
+
+def test_given_stream():
+    """Calls on a stream that is not the current one: their copies, allocations and zeroed workspaces belong to it."""
+    w = weight(512, 8192, "mx", 14, False)
+    big = rows(6, 8200, torch.float32, 15).cuda()
+    x = big[:, 1:8193]  # rows off 16-byte boundaries: copied
+    want = hq_fp4_linear(w, x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = [hq_fp4_linear(w, x, stream=s) for _ in range(20)]
+    q = hq_fp4_quantize(x, "mx", stream=s)
+    got += [hq_fp4_matmul(w, q, stream=s)]
+    s.synchronize()
+    assert all(torch.equal(g, want) for g in got)
 
 
 def test_rotated_basis():

@@ -137,6 +137,63 @@ def test_gradients_against_differences():
             assert abs(diff - d.view(-1)[i].item()) <= 1e-4
 
 
+class _Gather(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, plan):
+        ctx.plan = plan
+        return hq_moe_gather(x, plan, out=torch.zeros((plan.n_rows, x.shape[1]), dtype=x.dtype, device=x.device))
+
+    @staticmethod
+    def backward(ctx, g):
+        return hq_moe_gather_grad(g.contiguous(), ctx.plan), None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, w, plan):
+        ctx.plan = plan
+        ctx.save_for_backward(rows, w)
+        return hq_moe_combine(rows, plan, w)
+
+    @staticmethod
+    def backward(ctx, g):
+        rows, w = ctx.saved_tensors
+        drows, dw = hq_moe_combine_grad(g.contiguous(), rows, ctx.plan, w, out=torch.zeros_like(rows))
+        return drows, dw, None
+
+
+def test_expert_layer_trains_through_them():
+    """Sort, gather, each expert's own product, combine, as a training program joins them: outputs and all gradients
+    against the same layer written per token in 64 bits.  fp32 products of K terms: K 2^-24 of the sum of magnitudes
+    at most, here bounded through the largest values."""
+    T, k, E, H, F = 37, 3, 6, 24, 16
+    ids = routing(T, k, E, 5, 0.2)
+    plan = hq_moe_sort(torch.from_numpy(ids).cuda(), E, align=4)
+    x, w, W = rnd((T, H), torch.float32, 1), rnd((T, k), torch.float32, 2), rnd((E, H, F), torch.float32, 3)
+    dy = rnd((T, F), torch.float32, 4)
+    a = [v.cuda().requires_grad_() for v in (x, w, W)]
+    off, cnt = plan.offsets.tolist(), plan.counts.tolist()
+    xs = _Gather.apply(a[0], plan)
+    parts = [torch.zeros(0, F, device="cuda")]
+    for e in range(E):
+        rows_ = xs[off[e]:off[e + 1]]
+        parts.append(torch.tanh(rows_ @ a[2][e]) if off[e + 1] > off[e] else rows_.new_zeros(0, F))
+    z = torch.cat(parts)
+    z = torch.cat([z, z.new_zeros(plan.n_rows - z.shape[0], F)])
+    y = _Combine.apply(z, a[1], plan)
+    y.backward(dy.cuda())
+    b = [v.double().requires_grad_() for v in (x, w, W)]
+    want = torch.zeros(T, F, dtype=torch.float64)
+    for t in range(T):
+        for j in range(k):
+            if 0 <= ids[t, j] < E:
+                want[t] = want[t] + b[1][t, j] * torch.tanh(b[0][t] @ b[2][ids[t, j]])
+    want.backward(dy.double())
+    assert torch.allclose(y.detach().cpu().double(), want.detach(), rtol=0, atol=k * (H + 8) * 2.0**-22)
+    for got, ref in zip(a, b):
+        assert torch.allclose(got.grad.cpu().double(), ref.grad, rtol=0, atol=float(ref.grad.abs().max()) * (T * k + H) * 2.0**-22)
+
+
 def test_refusals():
     ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
     plan = hq_moe_sort(ids, 3)
