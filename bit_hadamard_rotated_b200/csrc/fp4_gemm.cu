@@ -82,6 +82,26 @@ __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t smem) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
+// L2 eviction policies for loads: gone first, kept.
+__device__ __forceinline__ uint64_t policy_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t policy_last() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+      "{%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // D (+)= (A sA) (B sB), K = 64, E2M1, A and B K-major in shared memory.
 template <int FMT>
 __device__ __forceinline__ void tc_mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
@@ -205,6 +225,7 @@ struct Item {
   int w_row;            // first weight row in the matrix
   int e;
   int c0, c1;  // chunks of K
+  bool more;   // grouped: another token tile takes these weights next
 };
 
 template <int NT, bool GROUPED>
@@ -262,6 +283,7 @@ struct Walk {
       it.w_row = e * a.M + it.m0;
       it.e = e;
       ++ni;
+      it.more = ni * NT < rows;
       ++u;
     } else {
       const int tile = u;
@@ -278,6 +300,7 @@ struct Walk {
       it.n_valid = min(NT, a.N - it.n0);
       it.w_row = it.m0;
       it.e = 0;
+      it.more = false;
     }
     return true;
   }
@@ -414,6 +437,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   bool ok = true;
 
   if (warp == 0) {
+    const uint64_t keep = policy_last(), gone = policy_first();
     if (a.early == 0) pdl_wait();
     if (FUSED) pdl_launch_dependents();
     Walk<NT, GROUPED> w(a, first);
@@ -430,10 +454,12 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         const size_t sf = (static_cast<size_t>(it.w_row >> 7) * a.wkb + c * S::kTiles) * 512;
         if (elect_one()) {
           mbar_arrive_expect_tx(full + slot, S::kW * (kWBytes + bytes));
-          tma_load_2d(p, &wmap, c * (kChunk / 2), it.w_row, full + slot);
+          const uint64_t pol = it.more ? keep : gone;
+          if (GROUPED) tma_load_2d_hint(p, &wmap, c * (kChunk / 2), it.w_row, full + slot, pol);
+          else tma_load_2d(p, &wmap, c * (kChunk / 2), it.w_row, full + slot);
           bulk_g2s(p + S::kSfOff, a.wsf + sf, bytes, full + slot);
           if constexpr (MODE == kGated) {
-            tma_load_2d(p + kWBytes, &wmap2, c * (kChunk / 2), it.w_row, full + slot);
+            tma_load_2d_hint(p + kWBytes, &wmap2, c * (kChunk / 2), it.w_row, full + slot, pol);
             bulk_g2s(p + S::kSfOff + S::kSf, a.wsf2 + sf, bytes, full + slot);
           }
         }
