@@ -1,5 +1,6 @@
-"""Run one hq_linear (or one MoE layer, KV attention or screened readout) case a
-few times on seeded synthetic inputs.
+"""Run one hq_linear (or one MoE layer, KV attention, screened readout, 4-bit
+floating-point linear or expert layer) case a few times on seeded synthetic
+inputs.
 
 A reproducible target for profilers and quick timing:
 
@@ -8,6 +9,8 @@ A reproducible target for profilers and quick timing:
     python -m bit_hadamard_rotated_b200.run_case --kv --tokens 8192
     python -m bit_hadamard_rotated_b200.run_case --readout
     python -m bit_hadamard_rotated_b200.run_case --M 8192 --K 8192 --batch 16 --tc-min-batch 1
+    python -m bit_hadamard_rotated_b200.run_case --fp4 nv --M 28672 --K 8192 --batch 1
+    python -m bit_hadamard_rotated_b200.run_case --fp4 mx --moe --batch 4096
 
 Inputs come from bit_hadamard_rotated_b200.synth (seeded); every call goes
 through the C ABI.  Prints the mean device time per call (CUDA events around
@@ -21,6 +24,7 @@ import numpy as np
 import torch
 
 from . import synth
+from .fp4 import Fp4Experts, Fp4Linear, Fp4Matrix, hq_fp4_quantize, hq_fp4_tensor_scale
 from .hq import (KVCache, RotatedLinear, ScreenedReadout, expert_table, hq_check_status, hq_moe_experts,
                  hq_moe_workspace_size)
 
@@ -127,6 +131,50 @@ def run_moe(a):
           f"({tb / (us * 1e-6) / 1e9:.0f} GB/s over {tb / 1e6:.1f} MB of touched expert weights)")
 
 
+def _fp4_weight(g, rows, K, fmt, dev):
+    w = torch.randn(rows, K, generator=g, device=dev) * K**-0.5
+    return hq_fp4_quantize(w, fmt, tensor_scale=hq_fp4_tensor_scale(w) if fmt == "nv" else None)
+
+
+def run_fp4(a):
+    """One packed 4-bit floating-point linear, bf16 activations (quantised in the call)."""
+    dev = torch.device("cuda", 0)
+    g = torch.Generator(device=dev).manual_seed(a.seed)
+    w = _fp4_weight(g, a.M, a.K, a.fp4, dev)
+    lin = Fp4Linear(w)
+    x = torch.randn(a.batch, a.K, generator=g, device=dev).bfloat16()
+    y = torch.empty(a.batch, a.M, dtype=torch.bfloat16, device=dev)
+    us = _timed(lambda: lin(x, out=y), a)
+    lin.check_status()
+    wb = w.codes.numel() + a.M * a.K // (16 if a.fp4 == "nv" else 32)
+    print(f"fp4 {a.fp4} linear M={a.M} K={a.K} batch {a.batch}: {us:.2f} us/call ({wb / (us * 1e-6) / 1e9:.0f} GB/s weights, "
+          f"{2.0 * a.M * a.K * a.batch / (us * 1e-6) / 1e12:.1f} TFLOP/s)")
+
+
+def run_fp4_experts(a):
+    """The packed expert layer: 256 experts, hidden 2048, intermediate 512, --batch tokens, top-8."""
+    E, H, I, k, T = 256, 2048, 512, 8, a.batch
+    dev = torch.device("cuda", 0)
+    g = torch.Generator(device=dev).manual_seed(a.seed)
+
+    def stack(rows, K):
+        m = _fp4_weight(g, E * rows, K, a.fp4, dev)
+        return Fp4Matrix(m.codes, m.scales, a.fp4, m.tensor_scale)
+
+    layer = Fp4Experts(stack(I, H), stack(I, H), stack(H, I), E)
+    x = torch.randn(T, H, generator=g, device=dev).bfloat16()
+    _, ids, w = synth.routing(synth._rng(a.seed, T, E, k), T, E, k)
+    ids, w = torch.from_numpy(ids).to(dev), torch.from_numpy(w).to(dev)
+    out = torch.empty_like(x)
+    us = _timed(lambda: layer(x, ids, w, out=out), a)
+    layer.check_status()
+    met = len(torch.unique(ids))
+    wb = met * 3 * (H * I // 2 + H * I // (16 if a.fp4 == "nv" else 32))
+    print(f"fp4 {a.fp4} experts E={E} hidden={H} inter={I} tokens={T} top-{k}: {us:.2f} us/call "
+          f"({wb / (us * 1e-6) / 1e9:.0f} GB/s over {wb / 1e6:.1f} MB of touched expert weights, "
+          f"{6.0 * T * k * H * I / (us * 1e-6) / 1e12:.1f} TFLOP/s)")
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawTextHelpFormatter)
     ap.add_argument("--M", type=int, default=12288)
@@ -138,6 +186,8 @@ def main():
     ap.add_argument("--warmup", type=int, default=3)
     ap.add_argument("--reps", type=int, default=3)
     ap.add_argument("--moe", action="store_true", help="run the MoE expert layer instead")
+    ap.add_argument("--fp4", choices=["nv", "mx"], help="4-bit floating-point weights of this format (with --moe: the "
+                    "expert layer on them, --batch tokens)")
     ap.add_argument("--kv", action="store_true", help="run the int4 KV attention instead")
     ap.add_argument("--tokens", type=int, default=8192, help="cached tokens for --kv")
     ap.add_argument("--readout", action="store_true", help="run the screened readout instead")
@@ -150,7 +200,9 @@ def main():
     from .hq import hq_set_gemv32_min_batch, hq_set_tc_min_batch
     hq_set_gemv32_min_batch(a.gemv32_min_batch)
     hq_set_tc_min_batch(a.tc_min_batch)
-    if a.moe:
+    if a.fp4:
+        (run_fp4_experts if a.moe else run_fp4)(a)
+    elif a.moe:
         run_moe(a)
     elif a.kv:
         run_kv(a)
