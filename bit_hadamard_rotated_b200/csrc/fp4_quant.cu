@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
 // The largest magnitude of a tensor over 2688 (= 6 * 448, the largest value
 // of a code times the largest block scale), 1 for an all-zero tensor.  Every
 // block folds its maximum into ws[0] (magnitudes order as their bit patterns;
-// a NaN's is above all), the last one writes the result and puts both words
-// back to zero.
+// a NaN's is above all), the last one writes the result.  Both words of ws are
+// zero at the start.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) tensor_scale_kernel(const T* __restrict__ x, size_t ldx, int rows,
                                                                 int chunks, float* __restrict__ out,
@@ -150,9 +150,8 @@ __global__ void __launch_bounds__(kThreads) tensor_scale_kernel(const T* __restr
     __threadfence();
     if (atomicAdd(ws + 1, 1u) == gridDim.x - 1) {
       __threadfence();
-      const float s = __fdiv_rn(__uint_as_float(atomicExch(ws, 0u)), 2688.f);
+      const float s = __fdiv_rn(__uint_as_float(atomicMax(ws, 0u)), 2688.f);
       *out = s == 0.f ? 1.f : s;
-      ws[1] = 0;
     }
   }
 }
@@ -264,6 +263,7 @@ hq_status hq_fp4_tensor_scale(const void* x, hq_dtype x_dtype, size_t ldx, int r
   const int grid = static_cast<int>(std::min<size_t>(blocks, static_cast<size_t>(sm_count()) * 8));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint32_t* ws = static_cast<uint32_t*>(workspace);
+  if (const cudaError_t e = cudaMemsetAsync(ws, 0, 2 * sizeof(uint32_t), st); e != cudaSuccess) return from_cuda(e);
   auto go = [&](auto* p) {
     using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
     return launch_pdl(fp4::tensor_scale_kernel<T>, dim3(grid), dim3(fp4::kThreads), 0, st, true, p, ldx, rows,

@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from ._lib import HQ_FP4_MX, HQ_FP4_NV, HqFp4Matrix, check, lib
-from .hq import _DT, _need_cuda, _on, _ptr, _raw_stream
+from .hq import _DT, _need_cuda, _new, _on, _ptr, _raw_stream
 
 _FMT = {"nv": HQ_FP4_NV, "mx": HQ_FP4_MX}
 
@@ -92,8 +92,8 @@ def hq_fp4_tensor_scale(x: torch.Tensor, stream=None) -> torch.Tensor:
 def _tensor_scale(x):
     dev = x.device
     x, ldx = _rows_in(x)
-    out = torch.empty((), dtype=torch.float32, device=dev)
-    ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+    out = torch.empty_strided((), (), dtype=torch.float32, device=dev)
+    ws = _new(1, 256, torch.uint8, dev)
     check(lib().hq_fp4_tensor_scale(x.data_ptr(), _DT[x.dtype], ldx, x.shape[0], x.shape[1],
                                     out.data_ptr(), ws.data_ptr(), 256, _raw_stream(None, dev.index)),
           "hq_fp4_tensor_scale")
@@ -104,7 +104,8 @@ def hq_fp4_quantize(x: torch.Tensor, fmt: str = "nv", tensor_scale: torch.Tensor
                     stream=None) -> Fp4Matrix:
     """Pack rows x [rows][K] (fp16/bf16/fp32, K a multiple of 32).  values: True,
     or a tensor like x to write into, for the rounded values in x's type too."""
-    _need_cuda(x, tensor_scale)
+    if not x.is_cuda:
+        _need_cuda(x)
     if fmt not in _FMT:
         raise ValueError('fmt must be "nv" or "mx"')
     _need_rows(x)
@@ -121,14 +122,17 @@ def hq_fp4_quantize(x: torch.Tensor, fmt: str = "nv", tensor_scale: torch.Tensor
 def _quantize(x, fmt, tensor_scale, values):
     dev, (rows, K) = x.device, x.shape
     x, ldx = _rows_in(x)
+    kb = -(-K // (64 if fmt == "nv" else 128))
     if values is True:
-        values = torch.empty_like(x, memory_format=torch.contiguous_format)
+        values = _new(rows, K, x.dtype, dev)
     elif values is False:
         values = None
     q = Fp4Matrix.__new__(Fp4Matrix)._set(
-        torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
-        torch.empty(_scale_shape(fmt, rows, K), dtype=torch.uint8, device=dev), fmt, tensor_scale, values)
-    q.c.K = K  # as given: an odd K is refused below
+        _new(rows, K // 2, torch.uint8, dev),
+        torch.empty_strided(_scale_shape(fmt, rows, K), (512 * kb, 512, 16, 4, 1), dtype=torch.uint8, device=dev), fmt,
+        tensor_scale, values)
+    if K & 1:
+        q.c.K = K  # as given: an odd K is refused below
     st = lib().hq_fp4_quantize(x.data_ptr(), _DT[x.dtype], ldx, q._ref,
                                None if values is None else values.data_ptr(), _raw_stream(None, dev.index))
     if st:
@@ -141,7 +145,7 @@ def _out(out, rows, M, dtype, dev):
     if dtype not in _DT:
         raise ValueError("the output must be fp16, bf16 or fp32")
     if out is None:
-        return torch.empty((rows, M), dtype=dtype, device=dev), M
+        return _new(rows, M, dtype, dev), M
     if out.dtype != dtype or tuple(out.shape) != (rows, M) or out.device != dev or (M > 1 and out.stride(1) != 1) \
             or (rows > 1 and out.stride(0) < M):
         raise ValueError(f"out must be {dtype} [{rows}][{M}] on {dev} with unit column stride")
@@ -307,7 +311,7 @@ class Fp4Experts(_Layer):
         x, ldx = _rows_in(x)
         ids, w = ids.contiguous(), w.contiguous()
         if out is None:
-            out = torch.empty((T, self.hidden), dtype=dtype, device=dev)
+            out = _new(T, self.hidden, dtype, dev)
         room = self._room
         if T > room[0] or k != room[1] or dtype != room[2]:
             self._grow(self._need(T, k, dtype), dev)

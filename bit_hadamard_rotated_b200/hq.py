@@ -46,6 +46,12 @@ def _on(dev, stream, fn, *args):
         return fn(*args)
 
 
+def _new(rows, cols, dtype, dev):
+    """An uninitialised [rows][cols] tensor (empty_strided costs the host about
+    two thirds of what torch.empty does)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=dev)
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:

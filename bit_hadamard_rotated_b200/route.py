@@ -9,7 +9,7 @@ from __future__ import annotations
 import torch
 
 from ._lib import check, lib
-from .hq import _DT, _need_cuda, _on, _raw_stream
+from .hq import _DT, _need_cuda, _new, _on, _raw_stream
 
 
 class MoePlan:
@@ -24,7 +24,7 @@ class MoePlan:
 
     @property
     def pos(self):
-        return self._buf[:self.T * self.k].view(self.T, self.k)
+        return self._buf.as_strided((self.T, self.k), (self.k, 1), 0)
 
     @property
     def offsets(self):
@@ -53,7 +53,7 @@ def _sort(ids, E, align, ws):
     # one allocation: pos, then offsets and counts, then the workspace, 256-byte aligned
     ends = (T * k + 63) // 64 * 64
     at = ends + (2 * max(E, 0) + 64) // 64 * 64
-    buf = torch.empty(at + (need // 4 if ws is None else 0), dtype=torch.int32, device=dev)
+    buf = torch.empty_strided((at + (need // 4 if ws is None else 0),), (1,), dtype=torch.int32, device=dev)
     plan = MoePlan(buf, T, k, E, ends, T * k + min(E, T * k) * (align - 1), align)
     p = plan._pos
     wp, wn = (p + 4 * at, need) if ws is None else (ws.data_ptr(), ws.numel())
@@ -93,7 +93,7 @@ def hq_moe_gather(x: torch.Tensor, plan: MoePlan, out: torch.Tensor | None = Non
 def _gather(x, plan, out):
     T, k = plan.T, plan.k
     if out is None:
-        out = torch.empty((plan.n_rows, x.shape[1]), dtype=x.dtype, device=x.device)
+        out = _new(plan.n_rows, x.shape[1], x.dtype, x.device)
     st = lib().hq_moe_gather(x.data_ptr(), _DT[x.dtype], plan._pos, T, k, x.shape[1], out.data_ptr(),
                              out.shape[0], _raw_stream(None, x.device.index))
     if st:
@@ -115,7 +115,7 @@ def _combine(rows, plan, topk_w, out_dtype, out, stream):
 def _launch_combine(rows, plan, topk_w, dt, out):
     T, k = plan.T, plan.k
     if out is None:
-        out = torch.empty((T, rows.shape[1]), dtype=dt, device=rows.device)
+        out = _new(T, rows.shape[1], dt, rows.device)
     st = lib().hq_moe_combine(rows.data_ptr(), _DT[rows.dtype], rows.shape[0], plan._pos,
                               None if topk_w is None else topk_w.data_ptr(), T, k, rows.shape[1], out.data_ptr(),
                               _DT[out.dtype], _raw_stream(None, rows.device.index))

@@ -422,8 +422,7 @@ hq_status hq_fp4_quantize(const void* x, hq_dtype x_dtype, size_t ldx, const hq_
 
 /* hq_fp4_tensor_scale -- *scale = max |x| / 2688 (6 * 448: the largest block
  * scale then meets the largest value), 1 where that is 0.  x as in
- * hq_fp4_quantize, rows >= 1.  workspace: 256 bytes, zero-filled before its
- * first use; calls leave it zero. */
+ * hq_fp4_quantize, rows >= 1.  workspace: 256 bytes, any contents. */
 hq_status hq_fp4_tensor_scale(const void* x, hq_dtype x_dtype, size_t ldx, int rows, int K, float* scale,
                               void* workspace, size_t ws_bytes, hq_stream_t stream);
 
