@@ -61,7 +61,11 @@ struct QuantArgs {
 };
 
 
-template <typename T, int FMT>
+// Where a row's codes go: to its own row; there with the rounded values; or to
+// the rows of the token's pairs.
+enum Target { kRows = 0, kValues = 1, kScatter = 2 };
+
+template <typename T, int FMT, int TARGET>
 __device__ __forceinline__ void quantize_piece(const QuantArgs& a, long row, int c, bool mine, const SixTs& ts,
                                                const Raw16<T>& raw) {
   const bool live = mine && row < a.rows && c * 16 < a.K;
@@ -76,17 +80,18 @@ __device__ __forceinline__ void quantize_piece(const QuantArgs& a, long row, int
   sw |= __shfl_xor_sync(~0u, sw, 2 << S);
   const bool scale_lane = mine && (c & ((4 << S) - 1)) == 0;
   const int st = c >> (2 + S);  // scale tile along K
-  if (a.pos == nullptr) {
-    if (live) *reinterpret_cast<uint2*>(a.codes + row * (a.K / 2) + c * 8) = p.codes;
+  if constexpr (TARGET != kScatter) {
+    const long o = row * a.K + c * 16;
+    if (live) *reinterpret_cast<uint2*>(a.codes + (o >> 1)) = p.codes;
     if (scale_lane && row < a.rows_pad) *reinterpret_cast<uint32_t*>(a.scales + scale_cell(row, st, a.kb)) = sw;
-    if (a.values != nullptr && live) {
+    if (TARGET == kValues && live) {
+      const uint64_t e2 = f2(p.eff, p.eff);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 f = from_e2m1x2((i < 4 ? p.codes.x : p.codes.y) >> (8 * (i & 3)));
-        v[2 * i] = f.x * p.eff;
-        v[2 * i + 1] = f.y * p.eff;
+        un2(mul2(f2(f.x, f.y), e2), v[2 * i], v[2 * i + 1]);
       }
-      store16<T>(static_cast<T*>(a.values) + row * a.K + c * 16, v);
+      store16<T>(static_cast<T*>(a.values) + o, v);
     }
   } else if (row < a.rows) {
     for (int j = 0; j < a.k; ++j) {
@@ -98,7 +103,7 @@ __device__ __forceinline__ void quantize_piece(const QuantArgs& a, long row, int
   }
 }
 
-template <typename T, int FMT>
+template <typename T, int FMT, int TARGET>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -115,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
     v.zero();
   }
   const SixTs ts(FMT == HQ_FP4_NV ? a.ts : nullptr);
-  quantize_piece<T, FMT>(a, row, c, mine, ts, v);
+  quantize_piece<T, FMT, TARGET>(a, row, c, mine, ts, v);
 }
 
 // The largest magnitude of a tensor over 2688 (= 6 * 448, the largest value
@@ -156,11 +161,17 @@ __global__ void __launch_bounds__(kThreads) tensor_scale_kernel(const T* __restr
   }
 }
 
+template <typename T, int FMT>
+cudaError_t quantize_launch(const QuantArgs& a, dim3 grid, cudaStream_t st) {
+  const dim3 block((a.cpb * a.rpb + 31) / 32 * 32);
+  if (a.pos != nullptr) return launch_pdl(quantize_rows_kernel<T, FMT, kScatter>, grid, block, 0, st, true, a);
+  return a.values != nullptr ? launch_pdl(quantize_rows_kernel<T, FMT, kValues>, grid, block, 0, st, true, a)
+                             : launch_pdl(quantize_rows_kernel<T, FMT, kRows>, grid, block, 0, st, true, a);
+}
+
 template <typename T>
 cudaError_t quantize_launch(int fmt, const QuantArgs& a, dim3 grid, cudaStream_t st) {
-  const dim3 block((a.cpb * a.rpb + 31) / 32 * 32);
-  return fmt == HQ_FP4_NV ? launch_pdl(quantize_rows_kernel<T, HQ_FP4_NV>, grid, block, 0, st, true, a)
-                          : launch_pdl(quantize_rows_kernel<T, HQ_FP4_MX>, grid, block, 0, st, true, a);
+  return fmt == HQ_FP4_NV ? quantize_launch<T, HQ_FP4_NV>(a, grid, st) : quantize_launch<T, HQ_FP4_MX>(a, grid, st);
 }
 
 }  // namespace
