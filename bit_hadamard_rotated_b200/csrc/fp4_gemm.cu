@@ -6,9 +6,9 @@
 //
 // tcgen05.mma takes E2M1 operands from shared memory and their block scales
 // from tensor memory and multiplies them in: no value is decoded anywhere.
-// Weights are the M side (128 rows a tile), tokens the N side (16 to 256), so
-// a token block of any size streams the weights once and the epilogue's lanes
-// run along an output row.
+// Weights are the M side (128 rows a tile), tokens the N side (32 to 128 of
+// one CTA, 256 of a pair), so a token block of any size streams the weights once
+// and the epilogue's lanes run along an output row.
 //
 // One CTA walks a list of (tile, K range) items.  Per 256 values of K it needs
 // 16 KB of weight codes (one TMA box, 128-byte swizzle), the tokens' codes,
@@ -21,8 +21,7 @@
 //   others   epilogue: tensor memory to registers, alpha, one rounding, y
 // The copies of the scales cost nothing beside the MMAs: 12 of them and 4 MMAs
 // of 256 tokens took 512 cycles, the MMAs' own time (through registers, by
-// four more warps, they took shared-memory bandwidth from the operands: 8192 x
-// 8192 at 4096 tokens 136 us instead of 121).
+// four more warps, they took shared-memory bandwidth from the operands).
 // Two accumulators where they fit (up to 128 tokens), so the next tile's MMAs
 // run under the epilogue.
 //
@@ -609,136 +608,136 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       if (lane == 0) mbar_arrive(tok_full);
     }
     if (warp >= S::kRoles + S::kTokWarps) {
-    const int ew = warp - S::kRoles - S::kTokWarps, quarter = warp & 3;
-    constexpr int kParts = S::kEpiWarps / 4;  // warps that share a lane quarter split the columns
-    const int col0 = (ew >> 2) * (NT / kParts), col1 = col0 + NT / kParts;
-    const int mrow = quarter * 32 + lane;
-    const SixTs hts(MODE == kGated ? a.hts : nullptr);
-    const float ats = a.ats != nullptr ? __ldg(a.ats) : 1.f;
-    Walk<NT, GROUPED> w(a, first);
-    Item it;
-    int acc = 0, accn = 0;
-    while (ok && w.next(a, it)) {
-      if (!warp_wait(dfull + acc, (accn / S::kAccs) & 1)) {
-        ok = false;
-        break;
-      }
-      tc::tc_fence_after();
-      const uint32_t d = tmem + acc * S::kW * NT + (static_cast<uint32_t>(quarter * 32) << 16);
-      const float alpha = (a.wts != nullptr ? __ldg(a.wts + (a.n_wts > 1 ? it.e : 0)) : 1.f) * ats;
-      const bool whole = it.c0 == 0 && it.c1 == a.C;
-      const int m = it.m0 + mrow;
-      if constexpr (MODE == kGated) {
-        // 16 tokens at a time: h of this lane's feature, a transpose through
-        // shared memory, then 16 features of one token per lane
-        const float alpha2 = (a.wts2 != nullptr ? __ldg(a.wts2 + (a.n_wts2 > 1 ? it.e : 0)) : 1.f) * ats;
-        float* buf = turn_buf + ew * 16 * kTurnRow;
-        // All of the warp's columns first, so that the next tile's MMAs can have
-        // the accumulators while h is computed and packed.
-        constexpr int kCols = NT / kParts;
-        float g[kCols], u[kCols];
-        if (col0 < it.n_valid) {
-          load_columns<kCols>(d + col0, g);
-          load_columns<kCols>(d + NT + col0, u);
+      const int ew = warp - S::kRoles - S::kTokWarps, quarter = warp & 3;
+      constexpr int kParts = S::kEpiWarps / 4;  // warps that share a lane quarter split the columns
+      const int col0 = (ew >> 2) * (NT / kParts), col1 = col0 + NT / kParts;
+      const int mrow = quarter * 32 + lane;
+      const SixTs hts(MODE == kGated ? a.hts : nullptr);
+      const float ats = a.ats != nullptr ? __ldg(a.ats) : 1.f;
+      Walk<NT, GROUPED> w(a, first);
+      Item it;
+      int acc = 0, accn = 0;
+      while (ok && w.next(a, it)) {
+        if (!warp_wait(dfull + acc, (accn / S::kAccs) & 1)) {
+          ok = false;
+          break;
         }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(dempty + acc);
-#pragma unroll
-        for (int c1 = 0; c1 < kCols; c1 += 16) {
-          const int c = col0 + c1;
-          if (c >= it.n_valid) break;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float x = g[c1 + i] * alpha;
-            buf[i * kTurnRow + lane] = __fdividef(x, 1.f + __expf(-x)) * (u[c1 + i] * alpha2);
+        tc::tc_fence_after();
+        const uint32_t d = tmem + acc * S::kW * NT + (static_cast<uint32_t>(quarter * 32) << 16);
+        const float alpha = (a.wts != nullptr ? __ldg(a.wts + (a.n_wts > 1 ? it.e : 0)) : 1.f) * ats;
+        const bool whole = it.c0 == 0 && it.c1 == a.C;
+        const int m = it.m0 + mrow;
+        if constexpr (MODE == kGated) {
+          // 16 tokens at a time: h of this lane's feature, a transpose through
+          // shared memory, then 16 features of one token per lane
+          const float alpha2 = (a.wts2 != nullptr ? __ldg(a.wts2 + (a.n_wts2 > 1 ? it.e : 0)) : 1.f) * ats;
+          float* buf = turn_buf + ew * 16 * kTurnRow;
+          // All of the warp's columns first, so that the next tile's MMAs can have
+          // the accumulators while h is computed and packed.
+          constexpr int kCols = NT / kParts;
+          float g[kCols], u[kCols];
+          if (col0 < it.n_valid) {
+            load_columns<kCols>(d + col0, g);
+            load_columns<kCols>(d + NT + col0, u);
           }
+          tc::tc_fence_before();
           __syncwarp();
-          const int tok = lane & 15, part = lane >> 4;
-          float v[16];
+          if (lane == 0) mbar_arrive(dempty + acc);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 f = *reinterpret_cast<const float4*>(buf + tok * kTurnRow + part * 16 + 4 * i);
-            v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+          for (int c1 = 0; c1 < kCols; c1 += 16) {
+            const int c = col0 + c1;
+            if (c >= it.n_valid) break;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x = g[c1 + i] * alpha;
+              buf[i * kTurnRow + lane] = __fdividef(x, 1.f + __expf(-x)) * (u[c1 + i] * alpha2);
+            }
+            __syncwarp();
+            const int token = lane & 15, part = lane >> 4;
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 f = *reinterpret_cast<const float4*>(buf + token * kTurnRow + part * 16 + 4 * i);
+              v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+            }
+            const Packed16 p = pack16<FMT>(v, top_of(v), hts, 16);
+            const uint32_t other = __shfl_xor_sync(~0u, p.byte, 16);
+            if (c + token < it.n_valid) {
+              const long row = it.n0 + c + token;
+              const int f0 = it.m0 + quarter * 32;  // the warp's first feature
+              *reinterpret_cast<uint2*>(a.h_codes + row * (a.M / 2) + (f0 + part * 16) / 2) = p.codes;
+              if (part == 0) {
+                if constexpr (FMT == HQ_FP4_NV) {
+                  uint8_t* s = a.h_scales + scale_cell(row, f0 >> 6, a.h_kb) + (quarter & 1) * 2;
+                  *reinterpret_cast<uint16_t*>(s) = static_cast<uint16_t>(p.byte | other << 8);
+                } else {
+                  a.h_scales[scale_cell(row, f0 >> 7, a.h_kb) + quarter] = static_cast<uint8_t>(p.byte);
+                }
+              }
+            }
+            __syncwarp();
           }
-          const Packed16 p = pack16<FMT>(v, top_of(v), hts, 16);
-          const uint32_t other = __shfl_xor_sync(~0u, p.byte, 16);
-          if (c + tok < it.n_valid) {
-            const long row = it.n0 + c + tok;
-            const int f0 = it.m0 + quarter * 32;  // the warp's first feature
-            *reinterpret_cast<uint2*>(a.h_codes + row * (a.M / 2) + (f0 + part * 16) / 2) = p.codes;
-            if (part == 0) {
-              if constexpr (FMT == HQ_FP4_NV) {
-                uint8_t* s = a.h_scales + scale_cell(row, f0 >> 6, a.h_kb) + (quarter & 1) * 2;
-                *reinterpret_cast<uint16_t*>(s) = static_cast<uint16_t>(p.byte | other << 8);
-              } else {
-                a.h_scales[scale_cell(row, f0 >> 7, a.h_kb) + quarter] = static_cast<uint8_t>(p.byte);
+        } else if (whole) {
+          constexpr int P = NT / kParts < 32 ? 16 : 32;
+          for (int c = col0; c < col1 && c < it.n_valid; c += P) {
+            float f[P];
+            load_columns<P>(d + c, f);
+            if (m < a.M) {
+#pragma unroll
+              for (int j = 0; j < P; ++j) f[j] *= alpha;
+              store_any<P>(a, it.n0 + c, m, f, it.n_valid - c);
+            }
+          }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(dempty + acc);
+        } else if constexpr (!GROUPED) {
+          const int tile = blockIdx.x / a.split;
+          constexpr size_t kPart = static_cast<size_t>(NT) * kM;
+          float* mine = a.part + blockIdx.x * kPart;
+          for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
+            float f[16];
+            load_columns<16>(d + c, f);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) __stcg(mine + (c + i) * kM + mrow, f[i]);
+          }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(dempty + acc);
+          // Each warp's share of the tile is counted on its own: the last of the
+          // tile's CTAs to bring it adds the parts, in their order.
+          uint32_t last = 0;
+          uint32_t* counter = a.counters + tile * kMaxEpiWarps + ew;
+          if (lane == 0 && col0 < it.n_valid) {
+            __threadfence();
+            last = atomicAdd(counter, 1u) == static_cast<uint32_t>(a.split - 1) ? 1u : 0u;
+          }
+          if (__shfl_sync(~0u, last, 0) != 0) {
+            __threadfence();
+            if (lane == 0) *counter = 0;
+            for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
+              float f[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) f[j] = 0.f;
+              for (int i = 0; i < a.split; ++i) {  // 16 loads in flight
+                const float* p = a.part + (static_cast<size_t>(tile) * a.split + i) * kPart + c * kM + mrow;
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = __ldcg(p + j * kM);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] += v[j];
+              }
+              if (m < a.M) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] *= alpha;
+                store_any<16>(a, it.n0 + c, m, f, it.n_valid - c);
               }
             }
           }
-          __syncwarp();
         }
-      } else if (whole) {
-        constexpr int P = NT / kParts < 32 ? 16 : 32;
-        for (int c = col0; c < col1 && c < it.n_valid; c += P) {
-          float f[P];
-          load_columns<P>(d + c, f);
-          if (m < a.M) {
-#pragma unroll
-            for (int j = 0; j < P; ++j) f[j] *= alpha;
-            store_any<P>(a, it.n0 + c, m, f, it.n_valid - c);
-          }
-        }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(dempty + acc);
-      } else if constexpr (!GROUPED) {
-        const int tile = blockIdx.x / a.split;
-        constexpr size_t kPart = static_cast<size_t>(NT) * kM;
-        float* mine = a.part + blockIdx.x * kPart;
-        for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
-          float f[16];
-          load_columns<16>(d + c, f);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) __stcg(mine + (c + i) * kM + mrow, f[i]);
-        }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(dempty + acc);
-        // Each warp's share of the tile is counted on its own: the last of the
-        // tile's CTAs to bring it adds the parts, in their order.
-        uint32_t last = 0;
-        uint32_t* counter = a.counters + tile * kMaxEpiWarps + ew;
-        if (lane == 0 && col0 < it.n_valid) {
-          __threadfence();
-          last = atomicAdd(counter, 1u) == static_cast<uint32_t>(a.split - 1) ? 1u : 0u;
-        }
-        if (__shfl_sync(~0u, last, 0) != 0) {
-          __threadfence();
-          if (lane == 0) *counter = 0;
-          for (int c = col0; c < col1 && c < it.n_valid; c += 16) {
-            float f[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = 0.f;
-            for (int i = 0; i < a.split; ++i) {  // 16 loads in flight
-              const float* p = a.part + (static_cast<size_t>(tile) * a.split + i) * kPart + c * kM + mrow;
-              float v[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = __ldcg(p + j * kM);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) f[j] += v[j];
-            }
-            if (m < a.M) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) f[j] *= alpha;
-              store_any<16>(a, it.n0 + c, m, f, it.n_valid - c);
-            }
-          }
-        }
+        ++accn;
+        acc = accn % S::kAccs;
       }
-      ++accn;
-      acc = accn % S::kAccs;
-    }
     }
   }
   if (!ok) record_error(a.status, HQ_DEV_TIMEOUT);

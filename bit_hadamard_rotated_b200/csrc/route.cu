@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
   pdl_launch_dependents();
   const int W = sort_warps(a.E), w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   count_tile(a, blockIdx.x, h);
-  int32_t carry = 0;  // aligned rows of the experts before this round
+  int32_t carry = 0;  // aligned rows of the experts before e0
   for (int e0 = 0; e0 < a.E; e0 += kSortThreads) {
     const int e = e0 + threadIdx.x;
     int total = 0, before = 0;

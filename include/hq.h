@@ -52,7 +52,9 @@
  *     the workspace are read only after it has finished.  Weights must
  *     therefore not be rewritten by the library call just before on the same
  *     stream (no library call writes them), and any other kernel or copy that
- *     writes them must complete, in stream order, before the call.
+ *     writes them must complete, in stream order, before the call.  (The
+ *     hq_fp4 and routing calls need no such care: a matrix may be packed by
+ *     the call just before the one that multiplies it.)
  *   - Alignment: packed weights, scales, activations and outputs must be
  *     16-byte aligned; the library checks this and returns
  *     HQ_ERR_INVALID_ARG otherwise.
