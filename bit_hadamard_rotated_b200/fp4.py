@@ -14,6 +14,7 @@ from ._lib import HQ_FP4_MX, HQ_FP4_NV, HqFp4Matrix, check, lib
 from .hq import _DT, _need_cuda, _new, _on, _ptr, _raw_stream
 
 _FMT = {"nv": HQ_FP4_NV, "mx": HQ_FP4_MX}
+_ZEROED = 8448  # bytes at a workspace's start, the status word and the counters: all of it that has to be zero
 
 
 def _scale_shape(fmt: str, rows: int, K: int):
@@ -154,8 +155,8 @@ def _out(out, rows, M, dtype, dev):
 
 def _workspace(ws, need, dev):
     if ws is None:
-        ws = torch.empty(max(need, 8448), dtype=torch.uint8, device=dev)
-        ws[:8448].zero_()  # the status word and the counters: all that has to be zero
+        ws = torch.empty(max(need, _ZEROED), dtype=torch.uint8, device=dev)
+        ws[:_ZEROED].zero_()
         return ws
     if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
@@ -230,9 +231,18 @@ class _Layer:
         self._ws = _workspace(None, need, dev)
 
     def check_status(self, stream=None):
-        """Raise HqError if a call on this layer recorded a device error."""
-        if self._ws is not None:
-            check(lib().hq_check_status(_ptr(self._ws), _raw_stream(stream, self._ws.device.index)), "device status")
+        """Raise HqError if a call on this layer, or a graph captured of one,
+        recorded a device error; the layer is ready for the next call then."""
+        for ws in (*self._outgrown, self._ws):
+            if ws is not None:
+                _on(ws.device, stream, self._check, ws)
+
+    @staticmethod
+    def _check(ws):
+        st = lib().hq_check_status(ws.data_ptr(), _raw_stream(None, ws.device.index))
+        if st:
+            ws[:_ZEROED].zero_()  # counters that the failed call left
+            check(st, "device status")
 
 
 class Fp4Linear(_Layer):

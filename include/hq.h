@@ -472,7 +472,7 @@ size_t hq_fp4_experts_workspace_size(const hq_fp4_matrix* gate, const hq_fp4_mat
  *   a    = q(x_t)                                 quantised once per token
  *   g, u = W_gate^e a,  W_up^e a                  for e = topk_ids[t][j], fp32
  *   h    = q(g / (1 + exp(-g)) * u)
- *   d    = W_down^e h                             rounded to y_dtype
+ *   d    = W_down^e h                             rounded to y_dtype (fp16: infinite beyond 65504)
  *   y_t  = sum_j topk_w[t][j] d_{t,j}             fp32, slots ascending, rounded
  * gate, up: [n_experts * inter] rows of K = hidden, down: [n_experts * hidden]
  * rows of K = inter, each expert's rows in a run; one format; hidden and inter

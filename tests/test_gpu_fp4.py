@@ -298,6 +298,51 @@ def test_captured_graph_outlives_a_larger_batch():
     assert torch.equal(layer(x), want)
 
 
+def test_layer_is_ready_again_after_a_device_error():
+    """A status word and counters as a call whose wait ran out leaves them, in the workspace in use and in one that a
+    captured graph still uses: reported, and the next call and replay are right."""
+    w = weight(512, 8192, "nv", 14, True)  # parts of K: arrivals are counted
+    layer = Fp4Linear(w)
+    x = rows(100, 8192, torch.bfloat16, 15).cuda()
+    small = layer(x[:30])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer(x[:30], out=small)
+    want, want_small = layer(x), hq_fp4_linear(w, x[:30])
+    layer.check_status()
+    assert len(layer._outgrown) == 1
+    for ws in (layer._ws, layer._outgrown[0]):
+        ws[:4].view(torch.int32).fill_(1)
+        ws[256:8448].view(torch.int32).fill_(1)
+        with pytest.raises(HqError):
+            layer.check_status()
+        layer.check_status()
+        small.zero_()
+        g.replay()
+        assert torch.equal(layer(x), want) and torch.equal(small, want_small)
+
+
+def test_two_layers_at_once():
+    """Pairs of CTAs, parts of K, one launch and two, on two streams."""
+    ws = [weight(4096, 8192, "nv", 16, True), weight(9600, 2048, "mx", 17, False)]
+    xs = [rows(n, w.K, torch.bfloat16, n).cuda() for w in ws for n in (1, 20, 700)]
+    want = [hq_fp4_linear(ws[i // 3], x) for i, x in enumerate(xs)]
+    layers = [Fp4Linear(w) for w in ws]
+    for i in (2, 5):
+        layers[i // 3](xs[i])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for i, x in enumerate(xs):
+            got.append((i, layers[i // 3](x, stream=streams[i // 3])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i, y in got)
+    for lay in layers:
+        lay.check_status()
+
+
 def test_given_stream():
     """Calls on a stream that is not the current one: their copies, allocations and zeroed workspaces belong to it."""
     w = weight(512, 8192, "mx", 14, False)
