@@ -205,7 +205,7 @@ struct GemmArgs {
   uint8_t* h_codes;
   uint8_t* h_scales;
   int h_kb;
-  int early;           // the weights (grouped: and the segments) may be read before the preceding kernel ends
+  int early;           // the weights may be read before the preceding kernel ends (grouped: always, and the segments)
   // fused: the tokens
   const void* x;
   int x_dtype;
@@ -317,33 +317,44 @@ struct Walk {
   }
 };
 
-// The experts' tiles and segments into shared memory, by the whole CTA.
-template <int NT>
-__device__ __forceinline__ void load_groups(const GemmArgs& a, int* first) {
+// The experts' tiles and segments into shared memory, by the whole CTA, a scan
+// over all threads (one warp's took 0.7 us for 256 experts, before the first
+// copy).  start, count: those of expert threadIdx.x.
+template <int NT, int THREADS>
+__device__ __forceinline__ void load_groups(const GemmArgs& a, int* first, int start, int count) {
+  __shared__ int sums[THREADS / 32];
   int* starts = first + a.E + 1;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    starts[e] = __ldg(a.offsets + e);
-    starts[a.E + e] = __ldg(a.counts + e);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int carry = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int n = e < a.E ? (starts[a.E + e] + NT - 1) / NT * a.mt : 0;
-      int s = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(~0u, s, o);
-        if (lane >= o) s += v;
-      }
-      if (e < a.E) first[e] = carry + s - n;
-      carry += __shfl_sync(~0u, s, 31);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int e0 = 0; e0 < a.E; e0 += THREADS) {
+    const int e = e0 + threadIdx.x;
+    if (e0 > 0 && e < a.E) {
+      start = __ldg(a.offsets + e);
+      count = __ldg(a.counts + e);
     }
-    if (lane == 0) first[a.E] = carry;
+    const int n = e < a.E ? (count + NT - 1) / NT * a.mt : 0;
+    int s = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(~0u, s, o);
+      if (lane >= o) s += v;
+    }
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    int before = carry;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      before += w < warp ? sums[w] : 0;
+      carry += sums[w];
+    }
+    if (e < a.E) {
+      first[e] = before + s - n;
+      starts[e] = start;
+      starts[a.E + e] = count;
+      if (e == a.E - 1) first[a.E] = before + s;
+    }
+    __syncthreads();
   }
-  __syncthreads();
 }
 
 // Rows y[0 .. n) of one column from P columns of a lane's accumulator.
@@ -420,6 +431,11 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(tok_full + 1);
   __shared__ int first[GROUPED ? 3 * kMaxGroups + 1 : 1];
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  int start = 0, count = 0;
+  if (GROUPED && threadIdx.x < a.E) {  // always early: see GemmArgs
+    start = __ldg(a.offsets + threadIdx.x);
+    count = __ldg(a.counts + threadIdx.x);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(full + i, S::kRoles - 1);
@@ -444,7 +460,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   tc::tc_fence_after();
   const uint32_t tmem = *tslot;
   const uint32_t sf_cols = tmem + S::kAccs * S::kW * NT;
-  if constexpr (GROUPED) load_groups<NT>(a, first);
+  if constexpr (GROUPED) load_groups<NT, S::kThreads>(a, first, start, count);
   bool ok = true;
 
   if (warp == 0) {
@@ -482,11 +498,11 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       }
     }
   } else if (!FUSED && warp == 2) {
+    Walk<NT, GROUPED> w(a, first);
     pdl_wait();
     // After the wait, so that whatever precedes this kernel is complete when
     // the next one starts.
     pdl_launch_dependents();
-    Walk<NT, GROUPED> w(a, first);
     Item it;
     int slot = 0, turn = 0, n = 0;
     while (ok && w.next(a, it)) {
