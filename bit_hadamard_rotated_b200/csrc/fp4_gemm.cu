@@ -88,26 +88,6 @@ __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t smem) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// L2 eviction policies for loads: gone first, kept.
-__device__ __forceinline__ uint64_t policy_first() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-__device__ __forceinline__ uint64_t policy_last() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-__device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
-                                                 uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
-      "{%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
-}
-
 // D (+)= (A sA) (B sB), K = 64, E2M1, A and B K-major in shared memory.
 template <int FMT>
 __device__ __forceinline__ void tc_mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
@@ -231,43 +211,51 @@ struct Item {
   int w_row;            // first weight row in the matrix
   int e;
   int c0, c1;  // chunks of K
-  bool more;   // grouped: another token tile takes these weights next
 };
 
-template <int NT, bool GROUPED>
+// A CTA's items.  Expert tiles count token tiles fastest.  The gated product
+// deals them out one by one, so that the CTAs that take a weight tile's other
+// uses, and an expert's tokens' other uses, run at the same time and find them
+// in L2: with an even run of tiles per CTA, whose second use of a weight tile
+// comes 6 us after the first, 4096 tokens read 427 MB for 340 and took 197 us,
+// 187 so.  The second product keeps its runs (its tiles have few chunks, and
+// the next tile of a run is found sooner: 32 tokens 53.6 us, dealt out 54.5).
+template <int NT, int MODE>
 struct Walk {
   int u, end;
-  const int* first;  // grouped: [E + 1] tiles before each expert, then [E] segment starts, [E] row counts
-  int e, ni, mi;     // grouped: the next tile
-  int rows, start;   // grouped: of expert e
+  const int* first;  // groups: [E + 1] tiles before each expert, then [E] segment starts, [E] row counts
+  int e, ni, mi;     // groups: the next tile (gated: an expert at or before its own)
+  int rows, start;   // groups: of expert e
   __device__ __forceinline__ Walk(const GemmArgs& a, const int* groups) : first(groups) {
-    if constexpr (GROUPED) {
-      // An even run of tiles per CTA, token tiles fastest: a weight tile's
-      // second use follows the first, before 36 us of other traffic have taken
-      // it out of L2 (with m tiles fastest, 4096 tokens read 533 MB for 340).
+    if constexpr (MODE == kGated) {
+      u = blockIdx.x;
+      end = uniform(first[a.E]);
+      e = 0;
+    } else if constexpr (MODE == kGrouped) {
       const long all = uniform(first[a.E]);
       u = static_cast<int>(all * blockIdx.x / gridDim.x);
       end = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
       e = 0;
-      int n = a.E;  // the expert whose tiles include u: first[e] <= u < first[e + 1]
-      while (n > 1) {
-        const int h = n >> 1;
-        if (uniform(first[e + h]) <= u) {
-          e += h;
-          n -= h;
-        } else {
-          n = h;
-        }
-      }
-      const int t = u - uniform(first[e]);
-      enter(a);
-      const int nts = max(1, (rows + NT - 1) / NT);
-      mi = t / nts;
-      ni = t - mi * nts;
+      if (u < end) find(a);
     } else {
       u = blockIdx.x / a.split;
       end = a.mt * a.nt;
     }
+  }
+  // The expert whose tiles include u, first[e] <= u < first[e + 1], from e on,
+  // 32 at a time, and u's place in it.
+  __device__ __forceinline__ void find(const GemmArgs& a) {
+    const int lane = threadIdx.x & 31;
+    while (true) {
+      const int i = e + 1 + lane;
+      const int n = __popc(__ballot_sync(~0u, i < a.E && first[i] <= u));
+      e += n;
+      if (n < 32) break;
+    }
+    enter(a);
+    const int t = u - uniform(first[e]), nts = (rows + NT - 1) / NT;
+    mi = t / nts;
+    ni = t - mi * nts;
   }
   __device__ __forceinline__ void enter(const GemmArgs& a) {
     rows = uniform(first[a.E + 1 + a.E + e]);
@@ -278,15 +266,21 @@ struct Walk {
     if (u >= end) return false;
     it.c0 = 0;
     it.c1 = a.C;
-    if constexpr (GROUPED) {
-      if (ni * NT >= rows) {
-        ni = 0;
-        ++mi;
-      }
-      while (mi >= a.mt || rows == 0) {  // the next expert that has rows
-        ++e;
-        enter(a);
-        ni = mi = 0;
+    if constexpr (MODE == kGated || MODE == kGrouped) {
+      if constexpr (MODE == kGated) {
+        find(a);
+        u += gridDim.x;
+      } else {
+        if (ni * NT >= rows) {
+          ni = 0;
+          ++mi;
+        }
+        while (mi >= a.mt || rows == 0) {  // the next expert that has rows
+          ++e;
+          enter(a);
+          ni = mi = 0;
+        }
+        ++u;
       }
       it.m0 = mi * kM;
       it.n0 = start + ni * NT;
@@ -294,8 +288,6 @@ struct Walk {
       it.w_row = e * a.M + it.m0;
       it.e = e;
       ++ni;
-      it.more = ni * NT < rows;
-      ++u;
     } else {
       const int tile = u;
       u += gridDim.x;  // parts: one per CTA
@@ -311,7 +303,6 @@ struct Walk {
       it.n_valid = min(NT, a.N - it.n0);
       it.w_row = it.m0;
       it.e = 0;
-      it.more = false;
     }
     return true;
   }
@@ -464,10 +455,9 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   bool ok = true;
 
   if (warp == 0) {
-    const uint64_t keep = policy_last(), gone = policy_first();
     if (a.early == 0) pdl_wait();
     if (FUSED) pdl_launch_dependents();
-    Walk<NT, GROUPED> w(a, first);
+    Walk<NT, MODE> w(a, first);
     Item it;
     int slot = 0, turn = 0, n = 0;
     while (ok && w.next(a, it)) {
@@ -481,12 +471,10 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         const size_t sf = (static_cast<size_t>(it.w_row >> 7) * a.wkb + c * S::kTiles) * 512;
         if (elect_one()) {
           mbar_arrive_expect_tx(full + slot, S::kW * (kWBytes + bytes));
-          const uint64_t pol = it.more ? keep : gone;
-          if (GROUPED) tma_load_2d_hint(p, &wmap, c * (kChunk / 2), it.w_row, full + slot, pol);
-          else tma_load_2d(p, &wmap, c * (kChunk / 2), it.w_row, full + slot);
+          tma_load_2d(p, &wmap, c * (kChunk / 2), it.w_row, full + slot);
           bulk_g2s(p + S::kSfOff, a.wsf + sf, bytes, full + slot);
           if constexpr (MODE == kGated) {
-            tma_load_2d_hint(p + kWBytes, &wmap2, c * (kChunk / 2), it.w_row, full + slot, pol);
+            tma_load_2d(p + kWBytes, &wmap2, c * (kChunk / 2), it.w_row, full + slot);
             bulk_g2s(p + S::kSfOff + S::kSf, a.wsf2 + sf, bytes, full + slot);
           }
         }
@@ -498,7 +486,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       }
     }
   } else if (!FUSED && warp == 2) {
-    Walk<NT, GROUPED> w(a, first);
+    Walk<NT, MODE> w(a, first);
     pdl_wait();
     // After the wait, so that whatever precedes this kernel is complete when
     // the next one starts.
@@ -532,7 +520,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
     }
   } else if (warp == 1) {
     const uint32_t d0 = uniform(tmem), sf0 = uniform(sf_cols), ring0 = uniform(smem_u32(ring));
-    Walk<NT, GROUPED> w(a, first);
+    Walk<NT, MODE> w(a, first);
     Item it;
     int slot = 0, par = 0, acc = 0, accn = 0, n = 0;
     if (FUSED) ok = warp_wait(tok_full, 0);
@@ -642,7 +630,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       const int mrow = quarter * 32 + lane;
       const SixTs hts(MODE == kGated ? a.hts : nullptr);
       const float ats = a.ats != nullptr ? __ldg(a.ats) : 1.f;
-      Walk<NT, GROUPED> w(a, first);
+      Walk<NT, MODE> w(a, first);
       Item it;
       int acc = 0, accn = 0;
       while (ok && w.next(a, it)) {
