@@ -1342,7 +1342,10 @@ cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, c
   if (e != cudaSuccess) return e;
   e = launch_quantize(l.fmt, xd, x, ldx, l.T, l.H, x_scale, ws + o.xc, ws + o.xs, nullptr, pos, l.k, rows, st);
   if (e != cudaSuccess) return e;
-  const int nt = static_cast<long>(l.T) * l.k > 48l * l.E ? 128 : 64;
+  // Token tiles: 256 experts x (2048, 512), top-8, 1024 / 2048 / 3000 / 4096
+  // tokens (32 to 128 an expert) 107 / 132.5 / 160 / 197 us with 64, 114 / 138 /
+  // 158 / 186 with 128.
+  const int nt = static_cast<long>(l.T) * l.k > 88l * l.E ? 128 : 64;
   const int box = nt == 128 ? Shape<HQ_FP4_NV, 128, kGated>::kBox : Shape<HQ_FP4_NV, 64, kGated>::kBox;
   const int grid = std::min(sm_count(), kMaxGrid);
   CUtensorMap wmap, wmap2, amap;

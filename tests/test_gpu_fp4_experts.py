@@ -178,6 +178,22 @@ def test_masked_tokens_get_zeros_and_repeats_are_equal():
     assert bool((layer(x, torch.from_numpy(ids).cuda(), a[1]) == 0).all())
 
 
+@pytest.mark.parametrize("T,k,E", [(900, 2, 1024), (23000, 4, 1000), (1, 1, 1024), (2000, 1, 700)])
+def test_many_experts_few_of_them_busy(T, k, E):
+    """More experts than threads, runs of empty ones at both ends and between, one with many tiles."""
+    H = I = 128
+    m = make(E, H, I, "nv", T)
+    layer = Fp4Experts(*m, E)
+    x = rnd((T, H), 6).bfloat16().cuda()
+    rng = np.random.default_rng(T)
+    ids = rng.choice([3, 360, 361, E - 2], (T, k), p=[0.1, 0.6, 0.2, 0.1]).astype(np.int32)
+    some = rng.random((T, k)) < 0.2
+    ids[some] = rng.integers(40, E - 40, some.sum()) // 3 * 3
+    w = rng.random((T, k)).astype(np.float32)
+    y = layer(x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda())
+    check_layer(layer, *m, E, x, ids, w, y)
+
+
 def test_one_expert_twice_in_a_token_and_all_tokens_to_one():
     E, H, I, T = 4, 128, 256, 33
     m = make(E, H, I, "mx")
