@@ -435,8 +435,8 @@ size_t hq_fp4_matmul_workspace_size(const hq_fp4_matrix* w, int n_rows);
 
 /*
  * hq_fp4_matmul -- y[n][m] = sum_k w[m][k] a[n][k] of two packed matrices of
- * one format and K, summed in fp32 by the tensor cores and rounded once to
- * y_dtype.  y: [a->rows][w->rows], row stride ldy elements (>= w->rows),
+ * one format and K, summed in fp32 by the tensor cores (in an order that
+ * depends on the sizes alone) and rounded once to y_dtype.  y: [a->rows][w->rows], row stride ldy elements (>= w->rows),
  * element-aligned.  a->rows = 0 launches nothing.
  */
 hq_status hq_fp4_matmul(const hq_fp4_matrix* w, const hq_fp4_matrix* a, void* y, hq_dtype y_dtype, size_t ldy,

@@ -396,3 +396,27 @@ def test_matmul_refusals():
         Fp4Matrix(w.codes, w.scales[:, :1].contiguous())
     n0 = hq_launch_count()
     assert hq_fp4_linear(w, torch.zeros(0, 256, device="cuda")).shape == (0, 128) and hq_launch_count() == n0
+
+
+def test_offsets_past_32_bits():
+    """Rows whose elements lie past 2^32, against the same rows on their own."""
+    R, K = 140000, 32768
+    x = torch.zeros(R, K, dtype=torch.bfloat16, device="cuda")
+    last = rows(300, K, torch.bfloat16, 18).cuda()
+    x[-300:] = last
+    x[5, 7] = 1.0
+    ts = hq_fp4_tensor_scale(x)
+    assert torch.equal(ts, hq_fp4_tensor_scale(last))
+    q, want = hq_fp4_quantize(x, tensor_scale=ts, values=True), hq_fp4_quantize(last, tensor_scale=ts, values=True)
+    assert torch.equal(q.codes[-300:], want.codes) and torch.equal(q.values[-300:], want.values)
+    w = weight(256, K, "nv", 19, True)  # codes and scales of tokens past 2^31 bytes
+    y = hq_fp4_matmul(w, q)
+    check_product(y[-300:], dense(w), dense(want), K)  # (300 rows on their own are summed in parts of K)
+    assert bool((y[6:-300] == 0).all())
+    del x, q, y
+
+    w, N = weight(16000, 64, "mx", 20, False), 300000
+    x = torch.zeros(N, 64, dtype=torch.bfloat16, device="cuda")
+    x[-300:] = rows(300, 64, torch.bfloat16, 21).cuda()
+    y = hq_fp4_linear(w, x)
+    assert torch.equal(y[-300:], hq_fp4_linear(w, x[-300:])) and bool((y[-500:-300] == 0).all())

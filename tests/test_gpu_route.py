@@ -228,3 +228,22 @@ def test_rows_outside_the_buffer_are_skipped():
     assert bool((guard[40:] == 3).all())
     full = hq_moe_gather(x, plan)
     assert torch.equal(out, full[:40])
+
+
+def test_offsets_past_32_bits():
+    """Rows whose elements lie past 2^32, forward and back."""
+    T, H, E = 300000, 15001, 3
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    x[-64:] = torch.randn(64, H, device="cuda").bfloat16()
+    ids = torch.full((T, 1), 1, dtype=torch.int32, device="cuda")
+    w = torch.full((T, 1), 0.5, device="cuda")
+    plan = hq_moe_sort(ids, E)
+    assert torch.equal(plan.pos[:, 0], torch.arange(T, dtype=torch.int32, device="cuda"))
+    xs = hq_moe_gather(x, plan)
+    assert torch.equal(xs[-64:], x[-64:]) and bool((xs[-200:-64] == 0).all())
+    y = hq_moe_combine(xs, plan, w)
+    assert torch.equal(y[-64:], (x[-64:].float() * 0.5).bfloat16())
+    dz, dw = hq_moe_combine_grad(x, xs, plan, w, out=y)
+    assert torch.equal(dz[-64:], (x[-64:].float() * 0.5).bfloat16())
+    want = (x[-64:].double() ** 2).sum(1)
+    assert bool(((dw[-64:, 0].double() - want).abs() <= (H / 32 + 5) * 2.0**-24 * want).all())
