@@ -54,6 +54,9 @@ constexpr int kMaxGroups = 1024;
 constexpr int kMaxEpiWarps = 8;   // of a kernel that splits tiles
 constexpr int kFusedTokens = 8;   // most tokens of a fused launch (one swizzle atom)
 constexpr int kSmemMax = 218 * 1024;  // dynamic; the experts' segments (12 KB) beside it
+// More than half an SM's shared memory: no two kernels that hold tensor memory
+// share an SM, or one that waits for the other's end could hold what it needs.
+constexpr int kSmemMin = 116 * 1024;
 
 // ------------------------------------------------------------------ PTX
 
@@ -154,6 +157,7 @@ struct Shape {
   static constexpr int kCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
   static_assert(kColsNeeded <= 512, "tensor memory");
   static_assert(kSlot % 1024 == 0, "swizzle atoms");
+  static_assert(MODE == kFused || kStages * kSlot >= kSmemMin, "one CTA per SM");
 };
 
 struct GemmArgs {
@@ -837,6 +841,7 @@ struct PairShape {
   static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = 32 * (3 + kEpiWarps);
   static_assert(NT + 2 * kSfCols <= 512, "tensor memory");
+  static_assert(kStages * kSlot >= kSmemMin, "one CTA per SM");
 };
 
 template <int FMT>
@@ -1134,7 +1139,8 @@ template <int FMT>
 cudaError_t fused_launch(const CUtensorMap& wmap, GemmArgs& a, int grid, cudaStream_t st) {
   using S = Shape<FMT, 32, kFused>;
   a.stages = fused_stages<FMT>(a.C);
-  const size_t smem = 1024 + static_cast<size_t>(a.stages) * S::kSlot + token_bytes<FMT>(a.C) + 512;
+  const size_t smem = std::max<size_t>(
+      kSmemMin, 1024 + static_cast<size_t>(a.stages) * S::kSlot + token_bytes<FMT>(a.C) + 512);
   return launch_pdl(gemm_kernel<FMT, 32, kFused>, dim3(grid), dim3(S::kThreads), smem, st, true, wmap, wmap, wmap, a);
 }
 
