@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const MoveArgs a) {
   }
 }
 
-// A warp per pair: out[pos] = w dy[t] and dw = <dy[t], z[pos]> (lanes' sums in
-// fp32, then a shuffle tree).  The k pairs of a token sit in neighbouring
+// A warp per pair: out[pos] = w dy[t] and dw = <dy[t], z[pos]> (four sums per
+// lane in fp32, then a shuffle tree).  The k pairs of a token sit in neighbouring
 // warps, so dy[t] is read from memory once.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const MoveArgs a) {
@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const MoveArgs a) {
     T* dz = static_cast<T*>(a.out) + static_cast<size_t>(r) * a.H;
     const float w = __ldg(a.w + pair);
     constexpr int U = VEC ? 4 : 8;  // pieces of both rows in flight
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
     for (int c0 = lane * N; c0 < a.H; c0 += 32 * N * U) {
       typename Piece<T, VEC>::Raw rg[U], rx[U];
 #pragma unroll
@@ -336,13 +337,14 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const MoveArgs a) {
           g.unpack(rg[u]);
           x.unpack(rx[u]);
 #pragma unroll
-          for (int i = 0; i < N; ++i) dot = fmaf(g.v[i], x.v[i], dot);
+          for (int i = 0; i < N; ++i) part[(VEC ? i : u) & 3] = fmaf(g.v[i], x.v[i], part[(VEC ? i : u) & 3]);
 #pragma unroll
           for (int i = 0; i < N; ++i) g.v[i] *= w;
           g.store(dz + c);
         }
       }
     }
+    dot = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
   }
