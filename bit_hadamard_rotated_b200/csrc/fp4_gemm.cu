@@ -1284,14 +1284,15 @@ struct Layer {
 
 // Workspace: [status, counters] [sort] [pos] [offsets, counts] [tokens' codes
 // and scales by expert row] [h's codes and scales] [d, the experts' outputs].
-// d has y's type if that is 16 bits (its rounding, half an ulp of each
-// expert's share, is of the size of y's own) and halves the traffic of the two
-// largest passes; fp32 for fp32 y.
+// d is fp32 whatever y's type: it is a partial result of each token's sum.  In
+// a 16-bit y's type (half the traffic of the two largest passes) bf16 results
+// were 1.4 times as far off as one rounding of them, and an fp16 d beyond
+// 65504 was infinite where the token's sum was not.
 struct LayerWs {
   size_t sort, pos, ends, xc, xs, hc, hs, d, bytes;
 };
 
-LayerWs layer_ws(const Layer& l, hq_dtype yd) {
+LayerWs layer_ws(const Layer& l) {
   LayerWs w{};
   size_t at = kStatusBytes + kCounterBytes;
   auto take = [&](size_t n) {
@@ -1307,7 +1308,7 @@ LayerWs layer_ws(const Layer& l, hq_dtype yd) {
   w.xs = take(scale_bytes(l.fmt, l.rows, l.H));
   w.hc = take(static_cast<size_t>(l.rows) * (l.I / 2));
   w.hs = take(scale_bytes(l.fmt, l.rows, l.I));
-  w.d = take(static_cast<size_t>(l.rows) * l.H * (yd == HQ_F32 ? 4 : 2));
+  w.d = take(static_cast<size_t>(l.rows) * l.H * sizeof(float));
   w.bytes = at;
   return w;
 }
@@ -1339,7 +1340,7 @@ cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, c
                            const Layer& l, const void* x, hq_dtype xd, size_t ldx, const int32_t* ids,
                            const float* topk_w, const float* x_scale, const float* h_scale, void* y, hq_dtype yd,
                            uint8_t* ws, cudaStream_t st) {
-  const LayerWs o = layer_ws(l, yd);
+  const LayerWs o = layer_ws(l);
   int32_t* pos = reinterpret_cast<int32_t*>(ws + o.pos);
   int32_t* offsets = reinterpret_cast<int32_t*>(ws + o.ends);
   int32_t* counts = offsets + l.E + 1;
@@ -1401,14 +1402,13 @@ cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, c
   a.mt = l.H / kM;
   a.C = (l.I + kChunk - 1) / kChunk;
   a.k_steps = l.I / 64;
-  const hq_dtype dd = yd;
   a.y = ws + o.d;
-  a.y_dtype = dd;
+  a.y_dtype = HQ_F32;
   a.ldy = l.H;
   e = l.fmt == HQ_FP4_NV ? group_launch<HQ_FP4_NV, kGrouped>(nt, wmap, wmap, amap, a, grid, st)
                          : group_launch<HQ_FP4_MX, kGrouped>(nt, wmap, wmap, amap, a, grid, st);
   if (e != cudaSuccess) return e;
-  return route::launch_combine(dd, yd, ws + o.d, pos, topk_w, y, l.T, l.k, l.H, rows, st);
+  return route::launch_combine(HQ_F32, yd, ws + o.d, pos, topk_w, y, l.T, l.k, l.H, rows, st);
 }
 
 size_t packed_bytes(int fmt, long rows, int K) {
@@ -1487,7 +1487,7 @@ size_t hq_fp4_experts_workspace_size(const hq_fp4_matrix* gate, const hq_fp4_mat
                                      int n_experts, int T, int k, hq_dtype y_dtype) {
   fp4::Layer l{};
   if (y_dtype < HQ_F16 || y_dtype > HQ_F32 || fp4::check_layer(gate, up, down, n_experts, T, k, l) != HQ_OK) return 0;
-  return fp4::layer_ws(l, y_dtype).bytes;
+  return fp4::layer_ws(l).bytes;
 }
 
 hq_status hq_fp4_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, const hq_fp4_matrix* down,
@@ -1506,7 +1506,7 @@ hq_status hq_fp4_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, con
   if (rows_ok != HQ_OK) return rows_ok;
   auto bad = [](const void* p, uintptr_t a) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; };
   if (bad(topk_ids, 4) || bad(topk_w, 4) || bad(y, 16)) return HQ_ERR_INVALID_ARG;
-  if (fp4::bad_workspace(workspace, ws_bytes, fp4::layer_ws(l, y_dtype).bytes)) return HQ_ERR_WORKSPACE;
+  if (fp4::bad_workspace(workspace, ws_bytes, fp4::layer_ws(l).bytes)) return HQ_ERR_WORKSPACE;
   return from_cuda(fp4::launch_experts(gate, up, down, l, x, x_dtype, ldx, topk_ids, topk_w, x_scale, h_scale, y,
                                        y_dtype, static_cast<uint8_t*>(workspace),
                                        reinterpret_cast<cudaStream_t>(stream)));

@@ -461,7 +461,7 @@ hq_status hq_fp4_linear(const hq_fp4_matrix* w, const void* x, hq_dtype x_dtype,
 int hq_fp4_linear_launches(const hq_fp4_matrix* w, int batch);
 
 /* Bytes of workspace hq_fp4_experts needs (0 on a bad argument); enough for
- * fewer tokens too. */
+ * fewer tokens too, and the same for every y_dtype. */
 size_t hq_fp4_experts_workspace_size(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, const hq_fp4_matrix* down,
                                      int n_experts, int T, int k, hq_dtype y_dtype);
 
@@ -472,7 +472,7 @@ size_t hq_fp4_experts_workspace_size(const hq_fp4_matrix* gate, const hq_fp4_mat
  *   a    = q(x_t)                                 quantised once per token
  *   g, u = W_gate^e a,  W_up^e a                  for e = topk_ids[t][j], fp32
  *   h    = q(g / (1 + exp(-g)) * u)
- *   d    = W_down^e h                             rounded to y_dtype (fp16: infinite beyond 65504)
+ *   d    = W_down^e h                             fp32
  *   y_t  = sum_j topk_w[t][j] d_{t,j}             fp32, slots ascending, rounded
  * gate, up: [n_experts * inter] rows of K = hidden, down: [n_experts * hidden]
  * rows of K = inter, each expert's rows in a run; one format; hidden and inter

@@ -243,3 +243,37 @@ def test_refusals():
         layer(x, torch.zeros((4, 33), dtype=torch.int32, device="cuda"), torch.zeros((4, 33), device="cuda"))
     n0 = hq_launch_count()
     assert layer(x[:0], ids[:0], w[:0]).shape == (0, 256) and hq_launch_count() == n0
+
+
+def test_outputs_are_rounded_once():
+    """A 16-bit y is the fp32 y rounded: each expert's output joins the weighted sum in fp32."""
+    E, H, I, T, k = 12, 512, 256, 90, 6
+    for fmt in ("nv", "mx"):
+        m = make(E, H, I, fmt, 21)
+        x = rnd((T, H), 22).bfloat16().cuda()
+        ids, w = (torch.from_numpy(v).cuda() for v in route(T, k, E, 23, 0.1))
+        want = Fp4Experts(*m, E, out_dtype=torch.float32)(x, ids, w)
+        for dt in (torch.bfloat16, torch.float16):
+            assert torch.equal(Fp4Experts(*m, E, out_dtype=dt)(x, ids, w), want.to(dt))
+
+
+def test_expert_outputs_beyond_fp16_whose_sum_is_within():
+    """Two experts of opposite down weights: each output passes 65504, the weighted sum does not."""
+    E, H, I, T = 2, 256, 128, 9
+    g, u = (rnd((I, H), s, H**-0.5) for s in (1, 2))
+    d = rnd((H, I), 3, 4e5 * I**-0.5)
+    def put(a, b):
+        parts = [hq_fp4_quantize(v.cuda(), "mx") for v in (a, b)]
+        return Fp4Matrix(torch.cat([p.codes for p in parts]), torch.cat([p.scales for p in parts]), "mx")
+    m = [put(g, g), put(u, u), put(d, -d)]
+    x = rnd((T, H), 4).half().cuda()
+    ids = torch.tensor([[0, 1]] * T, dtype=torch.int32, device="cuda")
+    one = Fp4Experts(*m, E, out_dtype=torch.float32)(x, ids[:, :1].contiguous(), torch.ones(T, 1, device="cuda"))
+    assert one.abs().max().item() > 65504
+    w = torch.tensor([[0.5, 0.499]] * T, device="cuda")
+    y = Fp4Experts(*m, E)(x, ids, w)
+    assert y.dtype == torch.float16 and bool(torch.isfinite(y).all())
+    want = one.double() * (w[:, :1].double() - w[:, 1:].double())
+    # two products of d and one sum in fp32 (2^-24 each of 0.5 |d| at most), one rounding to fp16
+    tol = 3 * 2.0**-24 * one.double().abs() + 2.0**-11 * want.abs() + 2.0**-25
+    assert bool(((y.double() - want).abs() <= tol).all())
