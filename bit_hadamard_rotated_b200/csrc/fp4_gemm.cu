@@ -669,8 +669,11 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
             if (c >= it.n_valid) break;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
+              if (c + i >= it.n_valid) break;
               const float x = g[c1 + i] * alpha;
-              buf[i * kTurnRow + lane] = __fdividef(x, 1.f + __expf(-x)) * (u[c1 + i] * alpha2);
+              // expf and an IEEE division, as in hq_moe_experts: the fast ones are off by up to
+              // 2 + 1.2 |g| ulps, enough to move h across a border between two codes.
+              buf[i * kTurnRow + lane] = x / (1.f + expf(-x)) * (u[c1 + i] * alpha2);
             }
             __syncwarp();
             const int token = lane & 15, part = lane >> 4;

@@ -277,3 +277,42 @@ def test_expert_outputs_beyond_fp16_whose_sum_is_within():
     # two products of d and one sum in fp32 (2^-24 each of 0.5 |d| at most), one rounding to fp16
     tol = 3 * 2.0**-24 * one.double().abs() + 2.0**-11 * want.abs() + 2.0**-25
     assert bool(((y.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("at", [-60.0, -20.0, 0.0, 12.0])
+def test_h_to_its_last_place(fmt, at):
+    """h = g / (1 + exp(-g)) u where the exponential is far from 1, read back through identity down matrices and fp32
+    outputs: y is 6 times the packed h.  Single-precision exp is within 1 ulp (2^-23), the sum, the quotient and the
+    product within half an ulp each: every packing of h (1 +- 2.6 2^-23) is allowed and no other."""
+    E, H, I, T = 2, 128, 128, 6000
+    rng = np.random.default_rng(int(at) + 100)
+    g, u = (hq_fp4_quantize(torch.from_numpy(v).float().cuda(), fmt) for v in
+            (at / H * (1 + 0.15 * rng.standard_normal((E * I, H))) + (0.05 if at == 0 else 0) * rng.standard_normal((E * I, H)),
+             rng.standard_normal((E * I, H)) * H**-0.5))
+    eye = hq_fp4_quantize(6 * torch.eye(128).repeat(E, 1).cuda(), fmt)
+    assert np.array_equal(dense(eye), np.tile(6 * np.eye(128), (E, 1)))
+    hs = None
+    if fmt == "nv":
+        hs = torch.tensor(abs(at / (1 + np.exp(-at)) if at else 0.5) / 1000, dtype=torch.float32, device="cuda")
+    x = torch.from_numpy(1 + 0.1 * rng.standard_normal((T, H))).float().cuda()
+    ids = torch.from_numpy(rng.integers(0, E, (T, 1)).astype(np.int32)).cuda()
+    y = bits(Fp4Experts(g, u, eye, E, h_scale=hs, out_dtype=torch.float32)(x, ids, torch.ones(T, 1, device="cuda"))).astype(np.float64)
+    t = 1.0 if hs is None else hs.item()
+    some = 0
+    for e in range(E):
+        r = np.flatnonzero(ids.cpu().numpy()[:, 0] == e)
+        a = hq_fp4_quantize(x[torch.from_numpy(r).cuda()], fmt)
+        gv, uv = (bits(hq_fp4_matmul(expert(m, e, I), a)).astype(np.float64) for m in (g, u))
+        h = gv / (1 + np.exp(-gv)) * uv
+        d = 2.6 * 2.0**-23 * np.abs(h)
+        hi, lo = np.abs(h) + d, np.maximum(np.abs(h) - d, 0)
+        # fp32 products of a code's value, its scale and the tensor scale: 2^-24 once more
+        ok = np.zeros(h.shape, dtype=bool)
+        for scale_from in (lo, hi):
+            for end in (h - d, h + d):
+                v = values_at(end, fmt, scale_from, t if fmt == "nv" else None)
+                ok |= np.abs(y[r] - 6 * v) <= 3 * 2.0**-24 * np.abs(6 * v)
+        some += int(np.count_nonzero(y[r]))
+        assert ok.all(), np.argwhere(~ok)[:5]
+    assert some > T * I / 4
