@@ -12,15 +12,17 @@
 namespace hq {
 namespace fp4 {
 
-// Whether 1 / b, and quotients by b, stay far from under- and overflow.
+// Whether 1 / b stays far from under- and overflow.
 __device__ __forceinline__ bool mid_range(float b) { return b >= 0x1p-100f && b <= 0x1p100f; }
 
-// x / b, correctly rounded, for x = 0 or of middling size like b and
+// x / b, correctly rounded up to 2^100 and above that at least 2^100 (every
+// scale saturates long before), for x = 0 or of middling size like b > 0 and
 // y = 1 / b correctly rounded: Markstein's quotient correction (IBM J. Res.
 // Dev. 34, 1990).  q = x y is within an ulp, and q + (x - q b) y, both steps
-// fused, rounds to the correctly rounded quotient.
+// fused, rounds to the correctly rounded quotient.  The bound on q keeps
+// x - q b from inf - inf where x y overflows.
 __device__ __forceinline__ float quotient(float x, float b, float y) {
-  const float q = __fmul_rn(x, y);
+  const float q = fminf(__fmul_rn(x, y), 0x1p100f);
   return __fmaf_rn(__fmaf_rn(-q, b, x), y, q);
 }
 
@@ -81,10 +83,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // x / eff for 16 values.  An E8M0 scale is a power of two and so is its
 // reciprocal (2^-125 to 2^127): one exact product.  Otherwise as quotient()
 // above, two values at a time, so that ties between codes are met exactly at 3
-// packed operations instead of two divisions.
+// packed operations instead of two divisions; where the block's largest
+// magnitude, amax, is far beyond its (saturated) scale, quotients could
+// overflow and are divided out.
 template <int FMT>
-__device__ __forceinline__ void quotients(float (&v)[16], float eff) {
-  if (FMT == HQ_FP4_MX || mid_range(eff)) {
+__device__ __forceinline__ void quotients(float (&v)[16], float amax, float eff) {
+  if (FMT == HQ_FP4_MX || (mid_range(eff) && amax <= __fmul_rn(eff, 0x1p20f))) {
     const float yf = FMT == HQ_FP4_MX ? __uint_as_float(static_cast<uint32_t>(
                                             254 - max(static_cast<int>(__float_as_uint(eff) >> 23), 0)) << 23)
                                       : __frcp_rn(eff);
@@ -156,7 +160,7 @@ __device__ __forceinline__ Packed16 pack16(float (&v)[16], uint32_t top, const S
     p.codes = make_uint2(0, 0);
     return p;
   }
-  quotients<FMT>(v, p.eff);
+  quotients<FMT>(v, __uint_as_float(top), p.eff);
   p.codes.x = to_e2m1x8(v);
   p.codes.y = to_e2m1x8(v + 8);
   return p;

@@ -420,3 +420,25 @@ def test_offsets_past_32_bits():
     x[-300:] = rows(300, 64, torch.bfloat16, 21).cuda()
     y = hq_fp4_linear(w, x)
     assert torch.equal(y[-300:], hq_fp4_linear(w, x[-300:])) and bool((y[-500:-300] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("amax,ts", [(1e30, 1e-10), (1e25, 1e-15), (2.0**122, 1e-5), (2.0**120, 2.0**-20), (2.0**100, 2.0**-99),
+                                     (3e38, 2.0**-30), (2.0**127, 2.0**-126), (2.0**60, 2.0**-90), (1e30, 1e-6)])
+def test_quantize_with_a_tensor_scale_far_too_small(dtype, amax, ts):
+    """Quotients past fp32's range: block scales end at 448, codes at 6 with the sign of x."""
+    ts = float(np.float32(ts))
+    x = np.zeros((5, 64))
+    x[0] = np.linspace(-1, 1, 64) * amax
+    x[1], x[1, 3], x[1, 40] = 0.0, -amax, amax  # one large value beside zeros
+    x[2] = np.linspace(1, -1, 64) * 2000 * ts    # within the scale's range
+    x[3, ::2], x[3, 1::2] = -amax, 3 * ts
+    x[4] = -amax * np.exp2(-np.arange(64.0))
+    x = torch.from_numpy(x).to(dtype)
+    q = hq_fp4_quantize(x.cuda(), "nv", tensor_scale=torch.tensor(ts, device="cuda"), values=dtype == torch.float32)
+    check_quantised(q, x, "nv", ts)
+    w = hq_fp4_quantize(rows(130, 64, torch.float32, 30, 0.1).cuda())
+    for n in (5, 2):  # quantised by the product's own CTAs, and by a kernel before it
+        big = x[:n].repeat(40 if n == 5 else 1, 1)
+        y = hq_fp4_linear(w, big.cuda(), x_scale=torch.tensor(ts, device="cuda"), out_dtype=torch.float32)
+        check_product(y, dense(w), fp4.quantize(big.double().numpy(), "nv", ts)[2], 64)
