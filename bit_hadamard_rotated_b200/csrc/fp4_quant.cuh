@@ -86,27 +86,35 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // packed operations instead of two divisions; where the block's largest
 // magnitude, amax, is far beyond its (saturated) scale, quotients could
 // overflow and are divided out.
+//
+// The corrected quotient is computed negated, -q = x (-y), then -q + (x - q b)
+// (-y), and the codes' signs are flipped back: for x = -0 the negated sum is
+// +0 - 0 = +0, so -0 again, where q + (x - q b) y would be -0 + 0 = +0.
+// Returns what the codes have to be xored with: their signs, or 0.
 template <int FMT>
-__device__ __forceinline__ void quotients(float (&v)[16], float amax, float eff) {
+__device__ __forceinline__ uint32_t quotients(float (&v)[16], float amax, float eff) {
   if (FMT == HQ_FP4_MX || (mid_range(eff) && amax <= __fmul_rn(eff, 0x1p20f))) {
     const float yf = FMT == HQ_FP4_MX ? __uint_as_float(static_cast<uint32_t>(
                                             254 - max(static_cast<int>(__float_as_uint(eff) >> 23), 0)) << 23)
-                                      : __frcp_rn(eff);
-    const uint64_t y = f2(yf, yf), n = f2(-eff, -eff);
+                                      : -__frcp_rn(eff);
+    const uint64_t y = f2(yf, yf), b = f2(eff, eff);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint64_t x = f2(v[2 * i], v[2 * i + 1]);
       uint64_t q = mul2(x, y);
-      if constexpr (FMT == HQ_FP4_NV) q = fma2(fma2(q, n, x), y, q);
+      if constexpr (FMT == HQ_FP4_NV) q = fma2(fma2(q, b, x), y, q);
       un2(q, v[2 * i], v[2 * i + 1]);
     }
-  } else if (eff > 0.f) {
+    return FMT == HQ_FP4_NV ? 0x88888888u : 0u;
+  }
+  if (eff > 0.f) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(v[i], eff);
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = copysignf(0.f, v[i]);
   }
+  return 0;
 }
 
 // Two values to two E2M1 codes (low nibble first), round to nearest even,
@@ -160,9 +168,9 @@ __device__ __forceinline__ Packed16 pack16(float (&v)[16], uint32_t top, const S
     p.codes = make_uint2(0, 0);
     return p;
   }
-  quotients<FMT>(v, __uint_as_float(top), p.eff);
-  p.codes.x = to_e2m1x8(v);
-  p.codes.y = to_e2m1x8(v + 8);
+  const uint32_t signs = quotients<FMT>(v, __uint_as_float(top), p.eff);
+  p.codes.x = to_e2m1x8(v) ^ signs;
+  p.codes.y = to_e2m1x8(v + 8) ^ signs;
   return p;
 }
 

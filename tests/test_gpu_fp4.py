@@ -442,3 +442,25 @@ def test_quantize_with_a_tensor_scale_far_too_small(dtype, amax, ts):
         big = x[:n].repeat(40 if n == 5 else 1, 1)
         y = hq_fp4_linear(w, big.cuda(), x_scale=torch.tensor(ts, device="cuda"), out_dtype=torch.float32)
         check_product(y, dense(w), fp4.quantize(big.double().numpy(), "nv", ts)[2], 64)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("ts", [None, 0.01])
+def test_zeros_keep_their_sign(fmt, dtype, ts):
+    """Negative zeros, and negative values that round to zero, beside values that do not."""
+    if fmt == "mx" and ts is not None:
+        pytest.skip("a tensor scale is NV's")
+    x = torch.zeros(6, 96, dtype=dtype)
+    x[0, ::3], x[0, 1::3] = -0.0, 1.5
+    x[1] = -0.0
+    x[1, 17] = -2.0
+    x[2, 1::2], x[2, ::2] = -1e-7, 3.0
+    x[3, ::2], x[3, 5] = -torch.finfo(dtype).tiny, 700.0
+    x[4] = -x[0]
+    x[5, 40] = 1.0
+    t = None if ts is None else torch.tensor(ts, device="cuda")
+    q = hq_fp4_quantize(x.cuda(), fmt, tensor_scale=t, values=True)
+    check_quantised(q, x, fmt, None if ts is None else float(np.float32(ts)))
+    got, want = q.values.cpu(), fp4.quantize(x.double().numpy(), fmt, ts)[2]
+    assert np.array_equal(torch.signbit(got).numpy(), np.signbit(want))
