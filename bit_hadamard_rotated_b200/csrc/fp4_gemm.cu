@@ -677,15 +677,19 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
             }
             __syncwarp();
             const int token = lane & 15, part = lane >> 4;
+            // (Rows without a token hold anything: as zeros they keep the warp from the
+            // quantiser's division, 32 tokens 51.2 us instead of 54.9.)
+            const bool there = c + token < it.n_valid;
             float v[16];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float4 f = *reinterpret_cast<const float4*>(buf + token * kTurnRow + part * 16 + 4 * i);
+              float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (there) f = *reinterpret_cast<const float4*>(buf + token * kTurnRow + part * 16 + 4 * i);
               v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
             }
             const Packed16 p = pack16<FMT>(v, top_of(v), hts, 16);
             const uint32_t other = __shfl_xor_sync(~0u, p.byte, 16);
-            if (c + token < it.n_valid) {
+            if (there) {
               const long row = it.n0 + c + token;
               const int f0 = it.m0 + quarter * 32;  // the warp's first feature
               *reinterpret_cast<uint2*>(a.h_codes + row * (a.M / 2) + (f0 + part * 16) / 2) = p.codes;
