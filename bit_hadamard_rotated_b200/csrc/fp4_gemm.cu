@@ -352,6 +352,23 @@ __device__ __forceinline__ void load_groups(const GemmArgs& a, int* first, int s
   }
 }
 
+// The two tensor scales of a product (nullptr: 1).  As one factor where their
+// product is a normal number (or one of them is 0); else one after the other,
+// the larger first, so that a result within fp32's range is not lost to a
+// product of scales that is infinite or has no bits left.
+struct Alpha {
+  float first, second;
+  __device__ __forceinline__ Alpha(float w, float t) {
+    const float p = fabsf(__fmul_rn(w, t));
+    const bool one = (p >= 0x1p-126f && p < INFINITY) || w == 0.f || t == 0.f;
+    const bool swap = fabsf(w) < fabsf(t);
+    first = one ? __fmul_rn(w, t) : swap ? t : w;
+    second = one ? 1.f : swap ? w : t;
+  }
+  __device__ __forceinline__ float operator()(float sum) const { return sum * first * second; }
+};
+__device__ __forceinline__ float scale_of(const float* p, int i) { return p != nullptr ? __ldg(p + i) : 1.f; }
+
 // Rows y[0 .. n) of one column from P columns of a lane's accumulator.
 template <int P, typename T>
 __device__ __forceinline__ void store_column(T* y, size_t ldy, const float (&f)[P], int n) {
@@ -633,24 +650,25 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       const int col0 = (ew >> 2) * (NT / kParts), col1 = col0 + NT / kParts;
       const int mrow = quarter * 32 + lane;
       const SixTs hts(MODE == kGated ? a.hts : nullptr);
-      const float ats = a.ats != nullptr ? __ldg(a.ats) : 1.f;
+      const float ats = scale_of(a.ats, 0);
       Walk<NT, MODE> w(a, first);
       Item it;
       int acc = 0, accn = 0;
       while (ok && w.next(a, it)) {
+        // before the wait, which hides the loads
+        const Alpha alpha(scale_of(a.wts, a.n_wts > 1 ? it.e : 0), ats);
+        const Alpha alpha2(MODE == kGated ? scale_of(a.wts2, a.n_wts2 > 1 ? it.e : 0) : 1.f, ats);
         if (!warp_wait(dfull + acc, (accn / S::kAccs) & 1)) {
           ok = false;
           break;
         }
         tc::tc_fence_after();
         const uint32_t d = tmem + acc * S::kW * NT + (static_cast<uint32_t>(quarter * 32) << 16);
-        const float alpha = (a.wts != nullptr ? __ldg(a.wts + (a.n_wts > 1 ? it.e : 0)) : 1.f) * ats;
         const bool whole = it.c0 == 0 && it.c1 == a.C;
         const int m = it.m0 + mrow;
         if constexpr (MODE == kGated) {
           // 16 tokens at a time: h of this lane's feature, a transpose through
           // shared memory, then 16 features of one token per lane
-          const float alpha2 = (a.wts2 != nullptr ? __ldg(a.wts2 + (a.n_wts2 > 1 ? it.e : 0)) : 1.f) * ats;
           float* buf = turn_buf + ew * 16 * kTurnRow;
           // All of the warp's columns first, so that the next tile's MMAs can have
           // the accumulators while h is computed and packed.
@@ -670,10 +688,10 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               if (c + i >= it.n_valid) break;
-              const float x = g[c1 + i] * alpha;
+              const float x = alpha(g[c1 + i]);
               // expf and an IEEE division, as in hq_moe_experts: the fast ones are off by up to
               // 2 + 1.2 |g| ulps, enough to move h across a border between two codes.
-              buf[i * kTurnRow + lane] = x / (1.f + expf(-x)) * (u[c1 + i] * alpha2);
+              buf[i * kTurnRow + lane] = x / (1.f + expf(-x)) * alpha2(u[c1 + i]);
             }
             __syncwarp();
             const int token = lane & 15, part = lane >> 4;
@@ -711,7 +729,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
             load_columns<P>(d + c, f);
             if (m < a.M) {
 #pragma unroll
-              for (int j = 0; j < P; ++j) f[j] *= alpha;
+              for (int j = 0; j < P; ++j) f[j] = alpha(f[j]);
               store_any<P>(a, it.n0 + c, m, f, it.n_valid - c);
             }
           }
@@ -756,7 +774,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
               }
               if (m < a.M) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] *= alpha;
+                for (int j = 0; j < 16; ++j) f[j] = alpha(f[j]);
                 store_any<16>(a, it.n0 + c, m, f, it.n_valid - c);
               }
             }
@@ -1015,7 +1033,7 @@ __global__ void __launch_bounds__(PairShape<FMT>::kThreads, 1)
     const int ew = warp - 3, quarter = warp & 3;
     const int col0 = (ew >> 2) * (NT / 2), col1 = col0 + NT / 2;
     const int mrow = quarter * 32 + lane;
-    const float alpha = (a.wts != nullptr ? __ldg(a.wts) : 1.f) * (a.ats != nullptr ? __ldg(a.ats) : 1.f);
+    const Alpha alpha(scale_of(a.wts, 0), scale_of(a.ats, 0));
     const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     int tile = 0;
     for (int t = pair; ok && t < tiles; t += pairs, ++tile) {
@@ -1036,7 +1054,7 @@ __global__ void __launch_bounds__(PairShape<FMT>::kThreads, 1)
         }
         if (m < a.M) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] *= alpha;
+          for (int j = 0; j < 32; ++j) f[j] = alpha(f[j]);
           store_any<32>(a, n0 + c, m, f, n_valid - c);
         }
       }

@@ -464,3 +464,29 @@ def test_zeros_keep_their_sign(fmt, dtype, ts):
     check_quantised(q, x, fmt, None if ts is None else float(np.float32(ts)))
     got, want = q.values.cpu(), fp4.quantize(x.double().numpy(), fmt, ts)[2]
     assert np.array_equal(torch.signbit(got).numpy(), np.signbit(want))
+
+
+@pytest.mark.parametrize("M,K,N", [(130, 64, 3), (300, 288, 40), (512, 16384, 100), (9473, 96, 400)])  # every kind of launch
+@pytest.mark.parametrize("ew,ea", [(66, 66), (-75, -75), (-100, -40), (100, -100), (-60, 120)])
+def test_tensor_scales_whose_product_leaves_fp32(M, K, N, ew, ea):
+    """Two tensor scales 2^ew and 2^ea, results within fp32's normal range, and rows of zeros, which stay zeros."""
+    size = 2.0**-9 if ew + ea > 100 else 256.0 if ew + ea < -100 else 1.0  # so that the results fit
+    rng = np.random.default_rng(M + N)
+    W = rng.integers(-4, 5, (M, K)) * 2.0**ew * size
+    X = rng.integers(-4, 5, (N, K)) * 2.0**ea * size
+    if ew + ea > 100:
+        W[:, 8:], X[:, 8:] = 0, 0
+    X[N // 2], W[M // 2] = 0, 0
+    tw, ta = (torch.tensor(2.0**e, dtype=torch.float32, device="cuda") for e in (ew, ea))
+    w = hq_fp4_quantize(torch.from_numpy(W).float().cuda(), tensor_scale=tw)
+    x = torch.from_numpy(X).float().cuda()
+    A = fp4.quantize(x.double().cpu().numpy(), "nv", 2.0**ea)[2]
+    want = A @ dense(w).T
+    y = hq_fp4_linear(w, x, x_scale=ta)
+    a = hq_fp4_quantize(x, tensor_scale=ta)
+    for got in (y, hq_fp4_matmul(w, a)):
+        got = got.double().cpu().numpy()
+        assert np.all(np.isfinite(got))
+        sums = (K + 64) * 2.0**-23 * (np.abs(A) @ np.abs(dense(w)).T)
+        assert np.all(np.abs(got - want) <= sums + 3 * 2.0**-24 * np.abs(want) + 3 * 2.0**-150)
+        assert np.any(got != 0)

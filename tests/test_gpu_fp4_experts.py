@@ -316,3 +316,30 @@ def test_h_to_its_last_place(fmt, at):
         some += int(np.count_nonzero(y[r]))
         assert ok.all(), np.argwhere(~ok)[:5]
     assert some > T * I / 4
+
+
+@pytest.mark.parametrize("ex,eg,eu,eh", [(-75, 46, -75, -133), (66, 66, 66, None)])
+def test_tensor_scales_whose_product_leaves_fp32(ex, eg, eu, eh):
+    """Tensor scales 2^ex of x and 2^eg, 2^eu of gate and up whose products are subnormal (u about 2^-122, h about as
+    large, h's own scale 2^eh) or infinite (g a large negative number, whose silu is 0); rows of zeros stay zeros."""
+    E, H, I, T = 2, 128, 128, 20
+    size = 2.0**-9 if ex > 0 else 512.0
+    rng = np.random.default_rng(5)
+    g, u = (rng.integers(-4, 5, (E * I, H)) * 2.0**e * size for e in (eg, eu))
+    dn, x = rng.integers(-4, 5, (E * H, I)) * 1.0, rng.integers(-4, 5, (T, H)) * 2.0**ex * size
+    if ex > 0:
+        g[:, 8:], u[:, 8:], x[:, 8:] = 0, 0, 0
+        g, x = -np.abs(g), np.abs(x)
+    x[3] = 0
+    m = []
+    for v, e in ((g, eg), (u, eu), (dn, 0)):
+        t = torch.full((), 2.0**e, device="cuda")
+        q = hq_fp4_quantize(torch.from_numpy(v).float().cuda(), "nv", tensor_scale=t)
+        m.append(Fp4Matrix(q.codes, q.scales, "nv", t.repeat(E)))
+    xs, hs = (None if e is None else torch.full((1,), 2.0**e, device="cuda") for e in (ex, eh))
+    ids, w = torch.from_numpy(rng.integers(0, E, (T, 1)).astype(np.int32)).cuda(), torch.ones(T, 1, device="cuda")
+    layer = Fp4Experts(*m, E, x_scale=xs, h_scale=hs, out_dtype=torch.float32)
+    x = torch.from_numpy(x).float().cuda()
+    y = layer(x, ids, w)
+    check_layer(layer, *m, E, x, ids.cpu().numpy(), w.cpu().numpy(), y, xs, hs)
+    assert bool((y[3] == 0).all()) and (bool((y == 0).all()) if eh is None else y.abs().max().item() > 2.0**-126)
