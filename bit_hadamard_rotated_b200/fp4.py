@@ -74,12 +74,13 @@ def _need_rows(x, K=None):
 
 def _rows_in(x):
     """x as rows the kernels read: unit stride along K and rows on 16-byte
-    boundaries (copied if they are not), and its row stride."""
+    boundaries (copied if they are not), and its row stride (of a contiguous x
+    its width: torch keeps any stride for a single row)."""
     if x.is_contiguous():
-        x = x if x.data_ptr() % 16 == 0 else x.clone()
-    elif x.stride(1) != 1 or x.stride(0) < x.shape[1] or x.stride(0) * x.element_size() % 16 or x.data_ptr() % 16:
-        x = x.contiguous()
-    return x, max(x.stride(0), x.shape[1])
+        return x if x.data_ptr() % 16 == 0 else x.clone(), x.shape[1]
+    if x.stride(1) != 1 or x.stride(0) < x.shape[1] or x.stride(0) * x.element_size() % 16 or x.data_ptr() % 16:
+        return x.contiguous(), x.shape[1]
+    return x, x.stride(0)
 
 
 def hq_fp4_tensor_scale(x: torch.Tensor, stream=None) -> torch.Tensor:

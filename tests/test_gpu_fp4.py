@@ -490,3 +490,21 @@ def test_tensor_scales_whose_product_leaves_fp32(M, K, N, ew, ea):
         sums = (K + 64) * 2.0**-23 * (np.abs(A) @ np.abs(dense(w)).T)
         assert np.all(np.abs(got - want) <= sums + 3 * 2.0**-24 * np.abs(want) + 3 * 2.0**-150)
         assert np.any(got != 0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_one_row_of_an_odd_pitch(dtype):
+    """A single row of a wider buffer, whose pitch is no multiple of 16 bytes, on and off 16-byte boundaries; a row of a
+    narrower one."""
+    w = weight(260, 512, "nv", 31, False)
+    big = rows(4, 513, dtype, 32).cuda()
+    for x in (big[:1, :512], big[1:2, :512], big[:1, 1:], big[3:, 1:], big.t().contiguous().t()[2:3, :512]):
+        c = x.clone(memory_format=torch.contiguous_format).reshape(-1).clone().reshape(1, 512)
+        a, b = hq_fp4_quantize(x), hq_fp4_quantize(c)
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+        assert torch.equal(hq_fp4_tensor_scale(x), hq_fp4_tensor_scale(c))
+        want = hq_fp4_matmul(w, b)
+        assert torch.equal(hq_fp4_linear(w, x, out_dtype=torch.float32), want)
+        assert torch.equal(Fp4Linear(w, out_dtype=torch.float32)(x), want)
+        flat = torch.as_strided(c, (1, 512), (1, 1))  # a pitch of 1
+        assert torch.equal(hq_fp4_linear(w, flat, out_dtype=torch.float32), want)

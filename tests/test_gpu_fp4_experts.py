@@ -343,3 +343,13 @@ def test_tensor_scales_whose_product_leaves_fp32(ex, eg, eu, eh):
     y = layer(x, ids, w)
     check_layer(layer, *m, E, x, ids.cpu().numpy(), w.cpu().numpy(), y, xs, hs)
     assert bool((y[3] == 0).all()) and (bool((y == 0).all()) if eh is None else y.abs().max().item() > 2.0**-126)
+
+
+def test_one_token_of_an_odd_pitch():
+    """A single row of a wider buffer whose pitch is no multiple of 16 bytes."""
+    E, H, I = 3, 256, 128
+    m = make(E, H, I, "nv", 9)
+    big = rnd((3, H + 1), 10).bfloat16().cuda()
+    ids, w = (torch.from_numpy(v).cuda() for v in route(1, 2, E, 11))
+    for x in (big[:1, :H], big[1:2, :H], big[:1, 1:]):
+        assert torch.equal(Fp4Experts(*m, E)(x, ids, w), Fp4Experts(*m, E)(x.repeat(2, 1)[:1], ids, w))
