@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from ._lib import HQ_FP4_MX, HQ_FP4_NV, HqFp4Matrix, check, lib
-from .hq import _DT, _need_cuda, _new, _on, _ptr, _raw_stream
+from .hq import _DT, _need_cuda, _need_workspace, _new, _on, _ptr, _raw_stream
 
 _FMT = {"nv": HQ_FP4_NV, "mx": HQ_FP4_MX}
 _ZEROED = 8448  # bytes at a workspace's start, the status word and the counters: all of it that has to be zero
@@ -159,8 +159,7 @@ def _workspace(ws, need, dev):
         ws = torch.empty(max(need, _ZEROED), dtype=torch.uint8, device=dev)
         ws[:_ZEROED].zero_()
         return ws
-    if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    _need_workspace(ws, dev)
     return ws
 
 

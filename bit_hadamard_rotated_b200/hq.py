@@ -58,6 +58,12 @@ def _need_cuda(*ts):
             raise ValueError("libhq takes CUDA tensors only (no CPU fallback)")
 
 
+def _need_workspace(ws, dev):
+    """A workspace that a caller gave: its bytes one after the other, on dev."""
+    if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+
+
 def hq_rotate(x: torch.Tensor, signs: torch.Tensor | None = None, out_dtype=torch.float32,
               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """x' = H_K diag(s) x / sqrt(K) for every row of x ([..., K])."""

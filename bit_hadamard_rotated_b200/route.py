@@ -9,7 +9,7 @@ from __future__ import annotations
 import torch
 
 from ._lib import check, lib
-from .hq import _DT, _need_cuda, _new, _on, _raw_stream
+from .hq import _DT, _need_cuda, _need_workspace, _new, _on, _raw_stream
 
 
 class MoePlan:
@@ -43,6 +43,8 @@ def hq_moe_sort(topk_ids: torch.Tensor, n_experts: int, align: int = 1, workspac
     _need_cuda(topk_ids, workspace)
     if topk_ids.dtype != torch.int32 or topk_ids.dim() != 2 or not topk_ids.is_contiguous():
         raise ValueError("topk_ids must be a contiguous int32 [T][k] tensor")
+    if workspace is not None:
+        _need_workspace(workspace, topk_ids.device)
     return _on(topk_ids.device, stream, _sort, topk_ids, int(n_experts), int(align), workspace)
 
 

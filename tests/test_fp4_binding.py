@@ -1,0 +1,53 @@
+"""The Python binding's own checks of the 4-bit floating-point and routing calls, on CPU tensors with a stand-in for the
+library that records what reaches it."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from bit_hadamard_rotated_b200 import fp4, hq, route
+
+
+class Recorder:
+    """Answers every size with 512 and every call with success."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_size"):
+            return lambda *a: 512
+        return lambda *a: self.calls.append((name, a)) or 0
+
+
+@pytest.fixture
+def rec(monkeypatch):
+    r = Recorder()
+    for mod in (fp4, route):
+        monkeypatch.setattr(mod, "lib", lambda: r)
+        monkeypatch.setattr(mod, "_need_cuda", lambda *ts: None)
+        monkeypatch.setattr(mod, "_raw_stream", lambda *a: 0)
+        monkeypatch.setattr(mod, "_on", lambda dev, stream, fn, *a: fn(*a))
+    return r
+
+
+def bytes_(n):
+    return torch.zeros(n, dtype=torch.uint8)
+
+
+BAD = {
+    "expanded": lambda: bytes_(1).expand(1 << 16),
+    "strided": lambda: bytes_(1 << 17)[::2],
+    "of another type": lambda: torch.zeros(1 << 16, dtype=torch.int32),
+    "of another device": lambda: torch.zeros(1 << 16, dtype=torch.uint8, device="meta"),
+}
+
+
+@pytest.mark.parametrize("how", BAD)
+def test_sort_refuses_workspaces(rec, how):
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        route.hq_moe_sort(ids, 8, workspace=BAD[how]())
+    assert rec.calls == []
+    route.hq_moe_sort(ids, 8, workspace=bytes_(1 << 16))
+    assert [n for n, _ in rec.calls] == ["hq_moe_sort"]
