@@ -154,12 +154,9 @@ def _out(out, rows, M, dtype, dev):
     return out, max(out.stride(0), M)
 
 
-def _workspace(ws, need, dev):
-    if ws is None:
-        ws = torch.empty(max(need, _ZEROED), dtype=torch.uint8, device=dev)
-        ws[:_ZEROED].zero_()
-        return ws
-    _need_workspace(ws, dev)
+def _workspace(need, dev):
+    ws = torch.empty(max(need, _ZEROED), dtype=torch.uint8, device=dev)
+    ws[:_ZEROED].zero_()
     return ws
 
 
@@ -169,13 +166,15 @@ def hq_fp4_matmul(w: Fp4Matrix, a: Fp4Matrix, out_dtype: torch.dtype = torch.flo
     dev = w.codes.device
     if a.codes.device != dev:
         raise ValueError(f"a is on {a.codes.device}, the weights on {dev}")
+    if workspace is not None:
+        _need_workspace(workspace, dev)
     return _on(dev, stream, _matmul, w, a, out_dtype, out, workspace)
 
 
 def _matmul(w, a, out_dtype, out, workspace):
     dev = w.codes.device
     out, ldy = _out(out, a.rows, w.rows, out_dtype if out is None else out.dtype, dev)
-    ws = _workspace(workspace, int(lib().hq_fp4_matmul_workspace_size(w._ref, a.rows)), dev)
+    ws = _workspace(int(lib().hq_fp4_matmul_workspace_size(w._ref, a.rows)), dev) if workspace is None else workspace
     check(lib().hq_fp4_matmul(w._ref, a._ref, out.data_ptr(), _DT[out.dtype], ldy, ws.data_ptr(), ws.numel(),
                               _raw_stream(None, dev.index)), "hq_fp4_matmul")
     return out
@@ -193,6 +192,8 @@ def hq_fp4_linear(w: Fp4Matrix, x: torch.Tensor, x_scale: torch.Tensor | None = 
     if x.device != dev:
         raise ValueError(f"x is on {x.device}, the weights on {dev}")
     _need_scale(x_scale, dev)
+    if workspace is not None:
+        _need_workspace(workspace, dev)
     dtype = out_dtype or (x.dtype if out is None else out.dtype)
     return _on(dev, stream, _linear, w, x, x_scale, dtype, out, workspace)
 
@@ -201,9 +202,7 @@ def _linear(w, x, x_scale, dtype, out, workspace):
     dev, N = w.codes.device, x.shape[0]
     x, ldx = _rows_in(x)
     out, ldy = _out(out, N, w.rows, dtype, dev)
-    ws = workspace
-    if ws is None or ws.device != dev or ws.dtype != torch.uint8:
-        ws = _workspace(ws, int(lib().hq_fp4_linear_workspace_size(w._ref, N)), dev)
+    ws = _workspace(int(lib().hq_fp4_linear_workspace_size(w._ref, N)), dev) if workspace is None else workspace
     st = lib().hq_fp4_linear(w._ref, x.data_ptr(), _DT[x.dtype], ldx, N,
                              None if x_scale is None else x_scale.data_ptr(), out.data_ptr(), _DT[dtype], ldy,
                              ws.data_ptr(), ws.numel(), _raw_stream(None, dev.index))
@@ -228,7 +227,7 @@ class _Layer:
         if self._ws is not None:
             self._outgrown.append(self._ws)
             need = max(need, 2 * self._ws.numel())
-        self._ws = _workspace(None, need, dev)
+        self._ws = _workspace(need, dev)
 
     def check_status(self, stream=None):
         """Raise HqError if a call on this layer, or a graph captured of one,

@@ -51,3 +51,19 @@ def test_sort_refuses_workspaces(rec, how):
     assert rec.calls == []
     route.hq_moe_sort(ids, 8, workspace=bytes_(1 << 16))
     assert [n for n, _ in rec.calls] == ["hq_moe_sort"]
+
+
+def matrix(rows, K):
+    return fp4.Fp4Matrix(torch.zeros(rows, K // 2, dtype=torch.uint8), torch.zeros(fp4._scale_shape("nv", rows, K), dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("how", BAD)
+def test_products_refuse_workspaces(rec, how):
+    w, a = matrix(128, 64), matrix(4, 64)
+    for call in (lambda ws: fp4.hq_fp4_linear(w, torch.zeros(4, 64), workspace=ws), lambda ws: fp4.hq_fp4_matmul(w, a, workspace=ws)):
+        rec.calls.clear()
+        with pytest.raises(ValueError):
+            call(BAD[how]())
+        assert rec.calls == []
+        call(bytes_(1 << 16))
+        assert len(rec.calls) == 1
