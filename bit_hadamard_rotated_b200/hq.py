@@ -38,6 +38,8 @@ def _on(dev, stream, fn, *args):
     as its current stream (so that what the call allocates, zeroes and copies
     belongs to the stream that it runs on)."""
     if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
         with torch.cuda.stream(stream):
             return fn(*args)
     if dev.index == torch.cuda.current_device():

@@ -67,3 +67,11 @@ def test_products_refuse_workspaces(rec, how):
         assert rec.calls == []
         call(bytes_(1 << 16))
         assert len(rec.calls) == 1
+
+
+def test_a_stream_of_another_device_is_refused():
+    """It would not be the one that the call runs on: launches go to the current stream of the tensors' device."""
+    ran = []
+    with pytest.raises(ValueError):
+        hq._on(torch.device("cuda", 0), SimpleNamespace(device=torch.device("cuda", 1)), ran.append, 1)
+    assert ran == []
