@@ -265,8 +265,10 @@ class Fp4Linear(_Layer):
     def _call(self, x, out):
         w, N = self.w, x.shape[0]
         if N > self._batch:
-            self._grow(int(lib().hq_fp4_linear_workspace_size(w._ref, N)), w.codes.device)
-            self._batch = N
+            need = int(lib().hq_fp4_linear_workspace_size(w._ref, N))
+            self._grow(need, w.codes.device)
+            if need:  # else the call below is refused
+                self._batch = N
         return _linear(w, x, self.x_scale, self.out_dtype or (x.dtype if out is None else out.dtype), out, self._ws)
 
 
@@ -323,8 +325,10 @@ class Fp4Experts(_Layer):
             out = _new(T, self.hidden, dtype, dev)
         room = self._room
         if T > room[0] or k != room[1] or dtype != room[2]:
-            self._grow(self._need(T, k, dtype), dev)
-            self._room = (T, k, dtype)
+            need = self._need(T, k, dtype)
+            self._grow(need, dev)
+            if need:  # else the call below is refused
+                self._room = (T, k, dtype)
         st = lib().hq_fp4_experts(self.gate._ref, self.up._ref, self.down._ref, self.n_experts, x.data_ptr(),
                                   _DT[x.dtype], ldx, T, ids.data_ptr(), w.data_ptr(), k,
                                   _ptr(self.x_scale), _ptr(self.h_scale), out.data_ptr(), _DT[dtype],

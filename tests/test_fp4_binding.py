@@ -5,7 +5,7 @@ from types import SimpleNamespace
 import pytest
 import torch
 
-from bit_hadamard_rotated_b200 import fp4, hq, route
+from bit_hadamard_rotated_b200 import HqError, fp4, hq, route
 
 
 class Recorder:
@@ -75,3 +75,38 @@ def test_a_stream_of_another_device_is_refused():
     with pytest.raises(ValueError):
         hq._on(torch.device("cuda", 0), SimpleNamespace(device=torch.device("cuda", 1)), ran.append, 1)
     assert ran == []
+
+
+class Sized(Recorder):
+    """Sizes that go by the batch, 0 (refused) beyond 1000; calls are refused with a workspace too small for them."""
+
+    def __getattr__(self, name):
+        def size(*a):
+            n = a[1] if name.startswith("hq_fp4_linear") else a[4]
+            return 0 if n > 1000 else 10000 + 100 * n
+
+        def call(*a):
+            self.calls.append((name, a))
+            n, room = (a[4], a[10]) if name == "hq_fp4_linear" else (a[7], a[16])
+            return 2 if n > 1000 else 3 if room < 10000 + 100 * n else 0
+        return size if name.endswith("workspace_size") else call
+
+
+def test_a_refused_batch_leaves_the_layer_as_it_was(rec, monkeypatch):
+    """A batch beyond the library's limits is refused; smaller ones still get their workspace."""
+    r = Sized()
+    monkeypatch.setattr(fp4, "lib", lambda: r)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: None)
+    lin = fp4.Fp4Linear(matrix(128, 64))
+    exp = fp4.Fp4Experts(matrix(256, 128), matrix(256, 128), matrix(256, 128), 2)
+
+    def experts(T):
+        return exp(torch.zeros(T, 128), torch.zeros(T, 2, dtype=torch.int32), torch.zeros(T, 2))
+    for call in (lambda n: lin(torch.zeros(n, 64)), experts):
+        call(4)
+        with pytest.raises(HqError):
+            call(2000)
+        for n in (3, 900, 500):
+            assert call(n).shape[0] == n
