@@ -212,22 +212,33 @@ def _linear(w, x, x_scale, dtype, out, workspace):
 
 
 class _Layer:
-    """A layer's workspace.  It grows with the calls; the ones it has outgrown
-    are kept, since a captured graph may still use them (each is at least twice
-    the one before)."""
+    """A layer's workspace.  It grows with the calls.  One that a graph was
+    captured on is kept when it is outgrown, and its successor is at least
+    twice as large; any other is given back."""
 
     def __init__(self):
-        self._ws, self._outgrown = None, []
+        self._ws, self._captured, self._outgrown = None, False, []
 
     def _grow(self, need, dev):
         if self._ws is not None and need <= self._ws.numel():
             return
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("call the layer once at this size before capturing it: its workspace has to grow")
-        if self._ws is not None:
-            self._outgrown.append(self._ws)
-            need = max(need, 2 * self._ws.numel())
+        old = self._ws
+        if old is not None and self._captured:
+            self._outgrown.append(old)
+            need = max(need, 2 * old.numel())
         self._ws = _workspace(need, dev)
+        if old is not None and not self._captured:
+            self._ws[:4].copy_(old[:4])  # the status of earlier calls
+            old.record_stream(torch.cuda.current_stream(dev))  # they may still be running
+        self._captured = False
+
+    def _room_for_call(self):
+        """The workspace as a call uses it."""
+        if not self._captured and torch.cuda.is_current_stream_capturing():
+            self._captured = True
+        return self._ws
 
     def check_status(self, stream=None):
         """Raise HqError if a call on this layer, or a graph captured of one,
@@ -269,7 +280,8 @@ class Fp4Linear(_Layer):
             self._grow(need, w.codes.device)
             if need:  # else the call below is refused
                 self._batch = N
-        return _linear(w, x, self.x_scale, self.out_dtype or (x.dtype if out is None else out.dtype), out, self._ws)
+        return _linear(w, x, self.x_scale, self.out_dtype or (x.dtype if out is None else out.dtype), out,
+                       self._room_for_call())
 
 
 class Fp4Experts(_Layer):
@@ -329,10 +341,11 @@ class Fp4Experts(_Layer):
             self._grow(need, dev)
             if need:  # else the call below is refused
                 self._room = (T, k, dtype)
+        ws = self._room_for_call()
         st = lib().hq_fp4_experts(self.gate._ref, self.up._ref, self.down._ref, self.n_experts, x.data_ptr(),
                                   _DT[x.dtype], ldx, T, ids.data_ptr(), w.data_ptr(), k,
                                   _ptr(self.x_scale), _ptr(self.h_scale), out.data_ptr(), _DT[dtype],
-                                  self._ws.data_ptr(), self._ws.numel(), _raw_stream(None, dev.index))
+                                  ws.data_ptr(), ws.numel(), _raw_stream(None, dev.index))
         if st:
             check(st, "hq_fp4_experts")
         return out

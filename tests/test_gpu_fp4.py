@@ -508,3 +508,65 @@ def test_one_row_of_an_odd_pitch(dtype):
         assert torch.equal(Fp4Linear(w, out_dtype=torch.float32)(x), want)
         flat = torch.as_strided(c, (1, 512), (1, 1))  # a pitch of 1
         assert torch.equal(hq_fp4_linear(w, flat, out_dtype=torch.float32), want)
+
+
+def test_outgrown_workspaces_are_given_back():
+    """Without a captured graph a layer holds the workspace of its largest call and no other, also when it grows on
+    another stream than the one that it started on, with calls still running."""
+    from bit_hadamard_rotated_b200 import fp4 as binding
+    w = weight(1024, 8192, "nv", 33, True)
+    big = rows(3000, 8192, torch.bfloat16, 34).cuda()
+    sizes = (20, 33, 100, 700, 1500, 3000)
+    want = [hq_fp4_linear(w, big[:n]) for n in sizes]
+    layer = Fp4Linear(w)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for i, n in enumerate(sizes):
+        here = torch.cuda.current_stream() if i % 2 == 0 else s
+        other = s if i % 2 == 0 else torch.cuda.current_stream()
+        for _ in range(8):
+            got.append((i, layer(big[:n], stream=here)))
+        other.wait_stream(here)
+        # what would take the workspace's memory if it were free for the stream that it came from
+        with torch.cuda.stream(other):
+            junk = [torch.full((layer._ws.numel(),), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        need = int(binding.lib().hq_fp4_linear_workspace_size(w._ref, n))
+        assert layer._ws.numel() == need and layer._outgrown == []
+        del junk
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i, y in got)
+    layer.check_status()
+
+
+def test_workspaces_of_captured_graphs_only_are_kept():
+    w = weight(1024, 8192, "nv", 35, True)
+    layer = Fp4Linear(w)
+    x = rows(900, 8192, torch.bfloat16, 36).cuda()
+    layer(x[:3])
+    y = layer(x[:40])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer(x[:40], out=y)
+    held = layer._ws
+    for n in (100, 400, 900):
+        layer(x[:n])
+    assert len(layer._outgrown) == 1 and layer._outgrown[0] is held
+    y.zero_()
+    g.replay()
+    assert torch.equal(y, hq_fp4_linear(w, x[:40]))
+
+
+def test_growing_keeps_the_status():
+    """A device error recorded before the workspace grew is still reported."""
+    w = weight(512, 8192, "nv", 37, True)
+    layer = Fp4Linear(w)
+    x = rows(300, 8192, torch.bfloat16, 38).cuda()
+    layer(x[:3])
+    layer._ws[:4].view(torch.int32).fill_(1)
+    layer(x)
+    with pytest.raises(HqError):
+        layer.check_status()
+    layer.check_status()
+    assert torch.equal(layer(x), hq_fp4_linear(w, x))
