@@ -84,6 +84,17 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(~0u, mbar_wait(bar, parity));
 }
 
+// The end of a warp that has filled a ring's slots in turn, n times in all:
+// waits (within the waits' limit) until its last copies have landed, which they
+// have on the usual path, since the MMAs waited for them; but no copy may be in
+// flight when a CTA that gave up a wait returns its shared memory.
+__device__ __forceinline__ bool drain_slots(uint64_t* full, int stages, int n) {
+  for (int i = max(0, n - stages); i < n; ++i) {
+    if (!warp_wait(full + i % stages, (i / stages) & 1)) return false;
+  }
+  return true;
+}
+
 // Scale tile (512 bytes) to four tensor-memory columns, in all four lane
 // quarters.
 __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t smem) {
@@ -196,6 +207,7 @@ struct GemmArgs {
   size_t ldx;
   int K;
   int stages;          // ring slots (beside them, the tokens of all of K)
+  int withhold;        // CTA 0 leaves its first weights' copy unrequested (hq_set_test_fault)
 };
 
 // Fused: shared memory of a chunk's tokens, 8 rows: codes (one swizzle atom)
@@ -440,7 +452,8 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
   uint64_t* dfull = empty + ST;
   uint64_t* dempty = dfull + S::kAccs;
   uint64_t* tok_full = dempty + S::kAccs;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(tok_full + 1);
+  uint64_t* drain = tok_full + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ int first[GROUPED ? 3 * kMaxGroups + 1 : 1];
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   int start = 0, count = 0;
@@ -458,6 +471,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       mbar_init(dempty + i, S::kEpiWarps);
     }
     mbar_init(tok_full, S::kTokWarps + S::kEpiWarps);
+    mbar_init(drain, 1);
     fence_mbar_init();
     prefetch_tensormap(&wmap);
     if (MODE == kGated) prefetch_tensormap(&wmap2);
@@ -492,7 +506,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         const size_t sf = (static_cast<size_t>(it.w_row >> 7) * a.wkb + c * S::kTiles) * 512;
         if (elect_one()) {
           mbar_arrive_expect_tx(full + slot, S::kW * (kWBytes + bytes));
-          tma_load_2d(p, &wmap, c * (kChunk / 2), it.w_row, full + slot);
+          if (a.withhold == 0 || blockIdx.x != 0 || n != 0) tma_load_2d(p, &wmap, c * (kChunk / 2), it.w_row, full + slot);
           bulk_g2s(p + S::kSfOff, a.wsf + sf, bytes, full + slot);
           if constexpr (MODE == kGated) {
             tma_load_2d(p + kWBytes, &wmap2, c * (kChunk / 2), it.w_row, full + slot);
@@ -506,6 +520,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         }
       }
     }
+    ok = drain_slots(full, ST, n) && ok;
   } else if (!FUSED && warp == 2) {
     Walk<NT, MODE> w(a, first);
     pdl_wait();
@@ -539,6 +554,7 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
         }
       }
     }
+    ok = drain_slots(full, ST, n) && ok;
   } else if (warp == 1) {
     const uint32_t d0 = uniform(tmem), sf0 = uniform(sf_cols), ring0 = uniform(smem_u32(ring));
     Walk<NT, MODE> w(a, first);
@@ -599,6 +615,9 @@ __global__ void __launch_bounds__(Shape<FMT, NT, MODE>::kThreads, 1)
       ++accn;
       acc = accn % S::kAccs;
     }
+    // no MMA may be in flight when tensor memory is freed
+    if (elect_one()) tc::tc_commit(drain);
+    ok = warp_wait(drain, 0) && ok;
   } else {
     pdl_wait();
     if constexpr (FUSED) {
@@ -881,7 +900,8 @@ __global__ void __launch_bounds__(PairShape<FMT>::kThreads, 1)
   uint64_t* empty = peer + ST;
   uint64_t* dfull = empty + ST;
   uint64_t* dempty = dfull + 1;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(dempty + 1);
+  uint64_t* drain = dempty + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = uniform(static_cast<int>(cluster_rank()));
   const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1, tiles = a.mt * a.nt;
@@ -893,6 +913,7 @@ __global__ void __launch_bounds__(PairShape<FMT>::kThreads, 1)
     }
     mbar_init(dfull, 1);
     mbar_init(dempty, 2 * S::kEpiWarps);
+    mbar_init(drain, 1);
     fence_mbar_init();
     prefetch_tensormap(&wmap);
     prefetch_tensormap(&amap);
@@ -926,7 +947,7 @@ __global__ void __launch_bounds__(PairShape<FMT>::kThreads, 1)
         const uint8_t* sf = a.wsf + (static_cast<size_t>(row >> 7) * a.wkb + c * S::kTiles) * 512;
         if (elect_one()) {
           mbar_arrive_expect_tx(full + slot, kWBytes + bytes);
-          tma_load_2d(p, &wmap, c * (kChunk / 2), row, full + slot);
+          if (a.withhold == 0 || blockIdx.x != 0 || n != 0) tma_load_2d(p, &wmap, c * (kChunk / 2), row, full + slot);
           if (bytes > 0) bulk_g2s(p + S::kSfOff, sf, bytes, full + slot);
         }
         ++n;
@@ -936,6 +957,7 @@ __global__ void __launch_bounds__(PairShape<FMT>::kThreads, 1)
         }
       }
     }
+    ok = drain_slots(full, ST, n) && ok;
   } else if (warp == 2) {
     pdl_wait();
     pdl_launch_dependents();  // after the wait, as in gemm_kernel
@@ -965,6 +987,7 @@ __global__ void __launch_bounds__(PairShape<FMT>::kThreads, 1)
         }
       }
     }
+    ok = drain_slots(full, ST, n) && ok;
   } else if (warp == 1 && rank != 0) {
     int slot = 0, par = 0;
     for (int t = pair; ok && t < tiles; t += pairs) {
@@ -980,6 +1003,7 @@ __global__ void __launch_bounds__(PairShape<FMT>::kThreads, 1)
         }
       }
     }
+    ok = warp_wait(drain, 0) && ok;  // the leader's MMAs read this CTA's slots
   } else if (warp == 1) {
     const uint32_t d = uniform(tmem), sf0 = uniform(sf_cols), ring0 = uniform(smem_u32(ring));
     int slot = 0, par = 0, n = 0, tile = 0;
@@ -1028,6 +1052,9 @@ __global__ void __launch_bounds__(PairShape<FMT>::kThreads, 1)
         }
       }
     }
+    // no MMA may be in flight when tensor memory is freed, in either CTA
+    if (elect_one()) pair_commit(drain);
+    ok = warp_wait(drain, 0) && ok;
   } else {
     pdl_wait();
     const int ew = warp - 3, quarter = warp & 3;
@@ -1238,6 +1265,7 @@ GemmArgs dense_args(const hq_fp4_matrix* w, const Plan& p, int N, void* y, hq_dt
   a.status = reinterpret_cast<uint32_t*>(ws);
   a.counters = reinterpret_cast<uint32_t*>(ws + kStatusBytes);
   a.part = reinterpret_cast<float*>(part);
+  a.withhold = take_test_fault() ? 1 : 0;
   return a;
 }
 
@@ -1411,6 +1439,7 @@ cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, c
   a.h_codes = ws + o.hc;
   a.h_scales = ws + o.hs;
   a.h_kb = scale_tiles(l.fmt, l.I);
+  a.withhold = take_test_fault() ? 1 : 0;
   e = l.fmt == HQ_FP4_NV ? group_launch<HQ_FP4_NV, kGated>(nt, wmap, wmap2, amap, a, grid, st)
                          : group_launch<HQ_FP4_MX, kGated>(nt, wmap, wmap2, amap, a, grid, st);
   if (e != cudaSuccess) return e;
@@ -1427,6 +1456,7 @@ cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, c
   a.mt = l.H / kM;
   a.C = (l.I + kChunk - 1) / kChunk;
   a.k_steps = l.I / 64;
+  a.withhold = 0;
   a.y = ws + o.d;
   a.y_dtype = HQ_F32;
   a.ldy = l.H;

@@ -632,8 +632,10 @@ int hq_set_gemv32_min_batch(int n);
  * then incomplete.  A 32-row GEMV launch that rotates its batch itself takes
  * one of the n instead: its CTA 0 does not publish its rotated row, so every
  * CTA's bounded wait at the rotation gate runs out the same way (the
- * workspace must then be zeroed again).  Nothing faults and the context stays
- * usable.  Returns the previous count; n < 0 only reads it. */
+ * workspace must then be zeroed again).  So does an hq_fp4 product (of
+ * hq_fp4_experts the first): its CTA 0 leaves its first copy of weights
+ * unrequested (the first 8448 bytes of the workspace must then be zeroed
+ * again).  Nothing faults and the context stays usable.  Returns the previous count; n < 0 only reads it. */
 int hq_set_test_fault(int n);
 
 #ifdef __cplusplus

@@ -91,3 +91,47 @@ def test_gemv32_gate_wait_runs_out_and_is_reported():
     hq_check_status(ws)
     want, bound = oracle.linear(bits, M, K, d["zero"], d["q"], d["scales"], d["signs"], d["x"], threads=8)
     assert np.all(np.abs(y - want) <= 2e-3 * bound + 1e-5)
+
+
+def _fp4_calls():
+    """A layer, its call and a second call that is the same work, for each kind of launch."""
+    from bit_hadamard_rotated_b200 import Fp4Experts, Fp4Linear, hq_fp4_quantize
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def rnd(*s):
+        return torch.randn(*s, device="cuda", generator=g)
+
+    def linear(M, K, N, fmt="nv"):
+        layer, x = Fp4Linear(hq_fp4_quantize(rnd(M, K) * K**-0.5, fmt)), rnd(N, K).bfloat16()
+        return layer, lambda: layer(x)
+
+    def experts(T):
+        E, H, I, k = 40, 1024, 256, 4
+        layer = Fp4Experts(*(hq_fp4_quantize(rnd(E * r, K) * K**-0.5, "mx") for r, K in ((I, H), (I, H), (H, I))), E)
+        x, ids = rnd(T, H).bfloat16(), torch.randint(0, E, (T, k), device="cuda", generator=g, dtype=torch.int32)
+        w = torch.rand(T, k, device="cuda", generator=g)
+        return layer, lambda: layer(x, ids, w)
+
+    return {"one launch": lambda: linear(4096, 4096, 1), "whole tiles": lambda: linear(4100, 4128, 60, "mx"),
+            "parts of K": lambda: linear(512, 16384, 100), "pairs": lambda: linear(9600, 4096, 400),
+            "experts": lambda: experts(33), "experts, large tiles": lambda: experts(2000)}
+
+
+@pytest.mark.parametrize("kind", ["one launch", "whole tiles", "parts of K", "pairs", "experts", "experts, large tiles"])
+def test_fp4_wait_runs_out_and_is_reported(kind):
+    """The packed products: CTA 0 leaves its first weights unrequested; every warp of that CTA (and of its pair) gives up,
+    its copies and MMAs in flight are waited for, the status says so, and the layer's next call is right."""
+    from bit_hadamard_rotated_b200 import HqError
+    from bit_hadamard_rotated_b200._lib import HQ_ERR_TIMEOUT, lib
+    layer, call = _fp4_calls()[kind]()
+    want = call()
+    layer.check_status()
+    assert lib().hq_set_test_fault(1) == 0
+    call()
+    with pytest.raises(HqError) as ei:
+        layer.check_status()
+    assert ei.value.status == HQ_ERR_TIMEOUT
+    assert lib().hq_set_test_fault(-1) == 0
+    for _ in range(3):
+        assert torch.equal(call(), want)
+    layer.check_status()
