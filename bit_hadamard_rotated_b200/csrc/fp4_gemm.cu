@@ -1201,8 +1201,7 @@ cudaError_t pair_launch(const CUtensorMap& wmap, const CUtensorMap& amap, const 
                         cudaStream_t st) {
   using S = PairShape<FMT>;
   const size_t smem = 1024 + static_cast<size_t>(S::kStages) * S::kSlot + 512;
-  cudaError_t e = cudaFuncSetAttribute(pair_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(pair_kernel<FMT>), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <mutex>
 
 #include "hq_internal.h"
 
@@ -16,6 +17,21 @@ static std::atomic<int> g_tc_min_batch{0};
 static std::atomic<int> g_g32_min_batch{0};
 
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+
+cudaError_t allow_smem(const void* kern, size_t bytes) {
+  struct Limit {
+    const void* kern;
+    size_t bytes;
+  };
+  constexpr size_t kTable = 2048;  // several times the library's kernels
+  static std::mutex lock;
+  static Limit table[kTable] = {};
+  const std::lock_guard<std::mutex> hold(lock);
+  size_t i = (reinterpret_cast<uintptr_t>(kern) >> 4) % kTable;
+  for (size_t n = 0; n < kTable && table[i].kern != nullptr && table[i].kern != kern; ++n) i = (i + 1) % kTable;
+  table[i] = {kern, table[i].kern == kern ? std::max(table[i].bytes, bytes) : bytes};
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(table[i].bytes));
+}
 
 // GEMV launches that still have to withhold one copy (hq_set_test_fault).
 static std::atomic<int> g_test_faults{0};

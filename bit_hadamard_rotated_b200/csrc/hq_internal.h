@@ -26,6 +26,12 @@ inline hq_status from_cuda(cudaError_t e) {
   return HQ_ERR_CUDA;
 }
 
+// Lets launches of a kernel have `bytes` of dynamic shared memory (more than 48
+// KiB).  The limit belongs to the kernel, not to a launch: it is never lowered,
+// so a call of another host thread that needs less cannot take it away between
+// this call and its launch.
+cudaError_t allow_smem(const void* kern, size_t bytes);
+
 // Counts every kernel launch libhq enqueues (hq_launch_count).
 void note_launch();
 // True (and one fewer pending) if hq_set_test_fault asked for a withheld copy.

@@ -570,3 +570,52 @@ def test_growing_keeps_the_status():
         layer.check_status()
     layer.check_status()
     assert torch.equal(layer(x), hq_fp4_linear(w, x))
+
+
+def test_two_host_threads():
+    """Layers of different widths (the fused launch's shared memory goes by K) and sorts of different numbers of
+    experts, called by two threads at once on their own streams."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    from bit_hadamard_rotated_b200 import hq_moe_sort
+    torch.cuda.synchronize()
+
+    def work(K, E):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            w = weight(128, K, "nv", K, False)
+            x = rows(1, K, torch.bfloat16, K).cuda()
+            layer = Fp4Linear(w)
+            ids = torch.arange(64, dtype=torch.int32, device="cuda").remainder(E).view(8, 8)
+            want, pos = layer(x).clone(), hq_moe_sort(ids, E).pos.clone()
+            good = torch.ones((), dtype=torch.bool, device="cuda")
+            for _ in range(1500):
+                y, p = layer(x), hq_moe_sort(ids, E).pos
+            good &= (y == want).all() & (p == pos).all()
+            return bool(good)
+
+    with ThreadPoolExecutor(2) as ex:
+        assert all(f.result() for f in [ex.submit(work, 256, 900), ex.submit(work, 8192, 16384)])
+
+
+def test_shared_memory_limits_of_two_host_threads():
+    """The C entry called in tight loops by four threads, with much and with little shared memory for one kernel."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    from bit_hadamard_rotated_b200._lib import lib
+    L = lib()
+
+    def work(E):
+        ids = torch.zeros(4, dtype=torch.int32, device="cuda")
+        out = torch.empty(4 + 2 * E + 1, dtype=torch.int32, device="cuda")
+        ws = torch.empty(L.hq_moe_sort_workspace_size(4, 1, E), dtype=torch.uint8, device="cuda")
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        p = out.data_ptr()
+        a = (ids.data_ptr(), 4, 1, E, 1, p, p + 16, p + 16 + 4 * (E + 1), ws.data_ptr(), ws.numel(), s.cuda_stream)
+        bad = sum(L.hq_moe_sort(*a) != 0 for _ in range(3000))
+        s.synchronize()
+        return bad, out[:4].tolist() == [0, 1, 2, 3]
+
+    with ThreadPoolExecutor(4) as ex:
+        assert list(ex.map(work, (900, 16384, 1000, 16000))) == [(0, True)] * 4
