@@ -2,11 +2,12 @@
 
 As everywhere in this package: checks of devices, types and shapes, pointer
 marshalling and the tensors' own device's current stream.  Nothing is computed
-here.
+here.  hq_moe_gather and hq_moe_combine take part in autograd.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._lib import check, lib
 from .hq import _DT, _need_cuda, _need_workspace, _new, _on, _raw_stream
@@ -83,10 +84,50 @@ def _need_weights(topk_w, plan):
     _need_like(topk_w, "topk_w", (plan.T, plan.k), torch.float32, plan.device)
 
 
+def _recorded(out):
+    """Whether autograd records a call on tensors that require a gradient."""
+    if out is not None and torch.is_grad_enabled():
+        raise ValueError("a call whose gradient is recorded takes no out")
+    return torch.is_grad_enabled()
+
+
+class _Gather(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, plan):
+        ctx.plan = plan
+        return _gather(x, plan, x.new_zeros((plan.n_rows, x.shape[1])))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        return hq_moe_gather_grad(g.contiguous(), ctx.plan), None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, topk_w, plan, out_dtype):
+        ctx.plan = plan
+        ctx.save_for_backward(rows, topk_w)
+        return _combine(rows, plan, topk_w, out_dtype, None, None)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        rows, topk_w = ctx.saved_tensors
+        dt = rows.dtype
+        if g.dtype != dt:  # fp32 from 16-bit rows or the other way round: nothing is rounded before the products
+            rows, g = rows.float(), g.float()
+        drows, dw = hq_moe_combine_grad(g.contiguous(), rows, ctx.plan, topk_w, out=torch.zeros_like(rows))
+        return drows.to(dt), dw, None, None
+
+
 def hq_moe_gather(x: torch.Tensor, plan: MoePlan, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Each token's row x[t] to the rows of its pairs: [n_rows][H] (rows without
-    a pair are left as they are in `out`; a new tensor's are not initialised)."""
+    a pair are left as they are in `out`; a new tensor's are not initialised, or
+    zero where x's gradient is recorded)."""
     _need_rows(x, "x", plan, True)
+    if x.requires_grad and _recorded(out):
+        return _on(x.device, stream, _Gather.apply, x, plan)
     if out is not None:
         _need_like(out, "out", (out.shape[0], x.shape[1]), x.dtype, x.device)
     return _on(x.device, stream, _gather, x, plan, out)
@@ -131,6 +172,8 @@ def hq_moe_combine(rows: torch.Tensor, plan: MoePlan, topk_w: torch.Tensor, out_
     """y[t] = sum_j topk_w[t][j] rows[pos[t][j]] (fp32 sums, slots ascending), of rows' type unless out_dtype says
     otherwise."""
     _need_weights(topk_w, plan)
+    if (rows.requires_grad or topk_w.requires_grad) and _recorded(out):
+        return _on(rows.device, stream, _Combine.apply, rows, topk_w, plan, out_dtype)
     return _combine(rows, plan, topk_w, out_dtype, out, stream)
 
 

@@ -247,3 +247,73 @@ def test_offsets_past_32_bits():
     assert torch.equal(dz[-64:], (x[-64:].float() * 0.5).bfloat16())
     want = (x[-64:].double() ** 2).sum(1)
     assert bool(((dw[-64:, 0].double() - want).abs() <= (H / 32 + 5) * 2.0**-24 * want).all())
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [(torch.float32, None), (torch.bfloat16, None), (torch.bfloat16, torch.float32),
+                                             (torch.float32, torch.float16)])
+@pytest.mark.parametrize("given", [False, True])
+def test_autograd_records_gather_and_combine(dtype, out_dtype, given):
+    """Gather, scale, combine under autograd, on the current stream and on a given one: the gradients of x, of the rows'
+    factor and of the weights against the formulas in 64 bits."""
+    T, k, E, H = 45, 4, 7, 72
+    ids = routing(T, k, E, 8, 0.2)
+    plan = hq_moe_sort(torch.from_numpy(ids).cuda(), E, align=8)
+    pos, _, _ = fp4.sort(ids, E, 8)
+    has = pos >= 0
+    x, w = rnd((T, H), dtype, 1).cuda().requires_grad_(), rnd((T, k), torch.float32, 2).cuda().requires_grad_()
+    f = rnd((plan.n_rows, H), dtype, 3).cuda().requires_grad_()
+    s = torch.cuda.Stream() if given else None
+    if given:
+        s.wait_stream(torch.cuda.current_stream())
+    xs = hq_moe_gather(x, plan, stream=s)
+    if given:
+        torch.cuda.current_stream().wait_stream(s)
+    z = xs * f
+    if given:
+        s.wait_stream(torch.cuda.current_stream())
+    y = hq_moe_combine(z, plan, w, out_dtype=out_dtype, stream=s)
+    if given:
+        torch.cuda.current_stream().wait_stream(s)
+    assert y.dtype == (out_dtype or dtype) and y.requires_grad
+    dy = rnd((T, H), y.dtype, 4).cuda()
+    y.backward(dy)
+    torch.cuda.synchronize()
+    free = np.setdiff1d(np.arange(plan.n_rows), pos[has])
+    assert bool((xs.detach()[free] == 0).all()) and bool((f.grad[free] == 0).all())
+    zd, dyd, wd = z.detach().double().cpu().numpy(), dy.double().cpu().numpy(), w.detach().double().cpu().numpy()
+    xd, fd = x.detach().double().cpu().numpy(), f.detach().double().cpu().numpy()
+    zp = np.where(has[..., None], zd[pos], 0)
+    near(y.detach(), (wd[..., None] * zp).sum(1), np.abs(wd[..., None] * zp).sum(1), y.dtype, 2 * k + 1)
+    near(w.grad, (dyd[:, None] * zp).sum(2), np.abs(dyd[:, None] * zp).sum(2), torch.float32, H + 5)
+    # dz is rounded to the rows' type, then times f and x in that type, then (x) summed over the slots
+    step = torch.finfo(dtype).eps / 2
+    t_of, j_of = np.nonzero(has)
+    dz = wd[has][:, None] * dyd[t_of]
+    df = dz * xd[t_of]
+    err = np.abs(f.grad.double().cpu().numpy()[pos[has]] - df)
+    assert np.all(err <= 3 * step * np.abs(df) + 2.0**-126)
+    dxs = np.zeros((T, k, H))
+    dxs[has] = dz * fd[pos[has]]
+    sums = np.abs(dxs).sum(1)
+    err = np.abs(x.grad.double().cpu().numpy() - dxs.sum(1))
+    assert np.all(err <= 3 * step * sums + k * 2.0**-24 * sums + step * np.abs(dxs.sum(1)) + 2.0**-126)
+
+
+def test_autograd_stays_out_of_it_where_nothing_is_recorded():
+    ids = routing(20, 2, 5, 9)
+    plan = hq_moe_sort(torch.from_numpy(ids).cuda(), 5)
+    x = torch.randn(20, 16, device="cuda").requires_grad_()
+    w = torch.rand(20, 2, device="cuda")
+    with torch.no_grad():
+        rows_ = hq_moe_gather(x, plan)
+        assert not rows_.requires_grad and not hq_moe_combine(rows_, plan, w.clone().requires_grad_()).requires_grad
+    assert not hq_moe_combine(rows_, plan, w).requires_grad
+    assert hq_moe_combine(rows_, plan, w.clone().requires_grad_()).requires_grad
+    with pytest.raises(ValueError):
+        hq_moe_gather(x, plan, out=torch.empty(plan.n_rows, 16, device="cuda"))
+    with pytest.raises(ValueError):
+        hq_moe_combine(rows_, plan, w.clone().requires_grad_(), out=torch.empty(20, 16, device="cuda"))
+    y = hq_moe_combine(hq_moe_gather(x, plan), plan, w)
+    (g,) = torch.autograd.grad(y.sum(), x, create_graph=True)  # once only: no second derivatives
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
