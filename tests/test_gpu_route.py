@@ -317,3 +317,17 @@ def test_autograd_stays_out_of_it_where_nothing_is_recorded():
     (g,) = torch.autograd.grad(y.sum(), x, create_graph=True)  # once only: no second derivatives
     with pytest.raises(RuntimeError):
         g.sum().backward()
+
+
+def test_plans_hold_every_routing():
+    """No segment ends past n_rows, which is reached where every expert has one pair."""
+    for T, k, E, align in ((16, 8, 128, 128), (3, 4, 40, 128), (33, 1, 32, 32), (7, 1, 7, 4096), (64, 2, 64, 2)):
+        ids = np.arange(T * k).reshape(T, k) % E
+        plan = hq_moe_sort(torch.from_numpy(ids.astype(np.int32)).cuda(), E, align=align)
+        end = int(plan.offsets[-1])
+        assert end <= plan.n_rows
+        pairs = np.bincount(ids.reshape(-1), minlength=E)
+        assert end == int((-(-pairs // align) * align).sum())
+        assert int(plan.pos.max()) < plan.n_rows
+    full = hq_moe_sort(torch.arange(128, dtype=torch.int32, device="cuda").view(16, 8), 128, align=128)
+    assert int(full.offsets[-1]) == full.n_rows == 128 * 128
