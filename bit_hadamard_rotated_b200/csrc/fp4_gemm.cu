@@ -74,8 +74,8 @@ __device__ __forceinline__ bool elect_one() {
 // A value that all lanes hold alike, by a reduction: its result is in a uniform
 // register, so the compiler knows that loops over it do not diverge.  Through a
 // shuffle it does not, and an expert tile's walk, waits and operands took 900
-// cycles a chunk instead of 650 (4096 tokens 205 us, 199.5 so; 32 tokens 59.3,
-// 56.4).
+// cycles a chunk instead of 650 (when it was changed, 4096 tokens 205 -> 199.5
+// us, 32 tokens 59.3 -> 56.4).
 __device__ __forceinline__ int uniform(int v) {
   return static_cast<int>(__reduce_or_sync(~0u, static_cast<unsigned>(v)));
 }
@@ -177,7 +177,7 @@ struct GemmArgs {
   const float* wts;
   const float* ats;
   int wkb;             // scale tiles along K
-  int a_row_tiles;     // token scale row tiles
+  int a_row_tiles;     // pairs: token scale row tiles
   int M, N, C;         // weight rows (of one expert), tokens, chunks of K
   int k_steps;         // MMAs of 64 over the whole of K
   int mt, nt;          // tiles
@@ -233,9 +233,10 @@ struct Item {
 // deals them out one by one, so that the CTAs that take a weight tile's other
 // uses, and an expert's tokens' other uses, run at the same time and find them
 // in L2: with an even run of tiles per CTA, whose second use of a weight tile
-// comes 6 us after the first, 4096 tokens read 427 MB for 340 and took 197 us,
-// 187 so.  The second product keeps its runs (its tiles have few chunks, and
-// the next tile of a run is found sooner: 32 tokens 53.6 us, dealt out 54.5).
+// comes 6 us after the first, it read 427 MB for 340, and the layer took 254 us
+// at 4096 tokens, 237 so.  The second product keeps its runs: its tiles have
+// few chunks, and the next tile of a run is found sooner (32 tokens 51.0 us,
+// dealt out 51.7; at 4096 tokens 237 and, dealt out, 229).
 template <int NT, int MODE>
 struct Walk {
   int u, end;
@@ -1106,6 +1107,7 @@ __global__ void __launch_bounds__(PairShape<FMT>::kThreads, 1)
 constexpr size_t kStatusBytes = 256;
 constexpr size_t kCounterBytes = 8192;  // a word per epilogue warp and CTA of a split grid
 constexpr int kMaxGrid = static_cast<int>(kCounterBytes / 4 / kMaxEpiWarps);
+static_assert(kStatusBytes + kCounterBytes == 8448, "what callers zero, in hq.h and the Python layers");
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
@@ -1117,11 +1119,12 @@ struct Plan {
 };
 
 // Parts of a tile's K are worth their exchange from about 8 chunks each on, for
-// more than 32 tokens from 16 and three parts.  2048 x 8192: 16 tokens 9.0 us
-// in 4 parts, 10.9 in 9, 11.9 whole; 128 tokens 14.2 us in 4 parts, 20 in 9,
-// 14.3 whole; 8192 x 8192: 64 tokens 16.4 us in 2 parts, 14.3 whole.  12288 x
-// 4096 at 16 (96 tiles of 148 CTAs): 8.9 us whole, 11.6 split evenly over all
-// CTAs.
+// more than 32 tokens from 16 and three parts.  2048 x 8192: 16 tokens 9.4 us
+// in 4 parts, 10.4 in 2, 10.8 in 9, 11.9 whole; 128 tokens 14.5 us in 4 parts,
+// 18.9 in 9, 14.0 whole.  2048 x 16384 at 128 tokens: 17.2 us in 4 parts, 19.5
+// in 2, 21.6 in 9, 23.4 whole.  8192 x 8192 at 64: 15.6 us in 2 parts, 13.3
+// whole.  (An even split of 96 tiles over all 148 CTAs, 12288 x 4096 at 16, was
+// slower too when it was tried: 11.6 us against 8.9 whole.)
 int parts_of(long tiles, long sms, int nt_size, int C) {
   const long s = std::min<long>(sms / tiles, C / (nt_size <= 32 ? 8 : 16));
   return static_cast<int>(s < (nt_size <= 32 ? 2 : 3) ? 1 : s);
@@ -1136,8 +1139,8 @@ Plan plan_of(int M, int N, int K) {
   p.nt = (N + p.nt_size - 1) / p.nt_size;
   const long tiles = static_cast<long>(p.mt) * p.nt;
   // More than one wave of 128 x 128 tiles: pairs.  4100 x 4128 at 333 tokens
-  // (99 tiles) 12.1 us, in pairs 13.6; 12288 x 4096 at 200 (192 tiles) 15.5 us,
-  // in pairs 12.1; 8192 x 8192 at 4096 129 us with 128 x 256 tiles, in pairs 115.
+  // (99 tiles) 11.8 us, in pairs 13.5; 12288 x 4096 at 200 (192 tiles) 15.3 us,
+  // in pairs 12.9; 8192 x 8192 at 4096 162 us, in pairs 115 (at full clock).
   if (N > 128 && tiles > sms) {
     p.pair = true;
     p.nt_size = 256;
@@ -1177,10 +1180,12 @@ int fused_stages(int C) {
   const long n = room / S::kSlot;
   return n < 4 ? 0 : static_cast<int>(std::min<long>(n, 8));
 }
-// One launch or two: every CTA quantises all of the tokens, 1.7 us per 8192
-// values, a kernel of its own costs about 2.5 us.  28672 x 8192: one token 27.5
-// against 30.2 us, two 30.2 against 29.9, eight 40 against 30; 4096 x 4096: two
-// tokens 9.5 against 11.4, eight 13.1 against 11.3.
+// One launch or two: every CTA quantises all of the tokens, about 1.7 us per
+// 8192 values, a kernel of its own costs about 2.5 us.  28672 x 8192: one token
+// 25.5 us against 26.5, two 28.2 against 26.3, eight 38.3 against 26.8; 4096 x
+// 4096: one 7.9 against 8.9, two 8.1 against 8.8, eight 11.9 against 8.8.
+// 12288 values are about even: one token of 4096 x 12288 11.8 against 12.2, of
+// 12288 x 12288 19.4 against 19.3, of 28672 x 12288 37.7 against 36.9.
 bool fused_fits(int fmt, int N, int K) {
   const int C = (K + kChunk - 1) / kChunk;
   return N <= kFusedTokens && static_cast<long>(N) * K <= 8192 &&
@@ -1402,8 +1407,10 @@ cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, c
   e = launch_quantize(l.fmt, xd, x, ldx, l.T, l.H, x_scale, ws + o.xc, ws + o.xs, nullptr, pos, l.k, rows, st);
   if (e != cudaSuccess) return e;
   // Token tiles: 256 experts x (2048, 512), top-8, 1024 / 2048 / 3000 / 4096
-  // tokens (32 to 128 an expert) 107 / 132.5 / 160 / 197 us with 64, 114 / 138 /
-  // 158 / 186 with 128.
+  // tokens (32 to 128 an expert) 120 / 155 / 195 / 248 us with 64, 131 / 160 /
+  // 197 / 238 with 128; 60 experts x (4096, 1024), top-4, 500 / 1000 / 1400 /
+  // 2000 tokens (33 to 133) 99 / 126 / 145 / 177 with 64, 109 / 125 / 147 / 171
+  // with 128.
   const int nt = static_cast<long>(l.T) * l.k > 88l * l.E ? 128 : 64;
   const int box = nt == 128 ? Shape<HQ_FP4_NV, 128, kGated>::kBox : Shape<HQ_FP4_NV, 64, kGated>::kBox;
   const int grid = std::min(sm_count(), kMaxGrid);
@@ -1416,7 +1423,6 @@ cudaError_t launch_experts(const hq_fp4_matrix* gate, const hq_fp4_matrix* up, c
   a.offsets = offsets;
   a.counts = counts;
   a.E = l.E;
-  a.a_row_tiles = rows / kM;
 
   if ((e = code_map(&wmap, gate->codes, gate->rows, l.H, kM)) != cudaSuccess) return e;
   if ((e = code_map(&wmap2, up->codes, up->rows, l.H, kM)) != cudaSuccess) return e;

@@ -9,7 +9,8 @@
 namespace hq {
 namespace route {
 
-// Workspace of a sort: [256 bytes, unused] [a histogram per tile of pairs].
+// Workspace of a sort: a histogram per tile of pairs, if there is more than one
+// tile (and 256 bytes in front, since a size of 0 is a bad argument's).
 size_t sort_workspace_bytes(long pairs, int E);
 int sort_launches(long pairs);
 bool sort_supported(long pairs, int E, int align);

@@ -476,8 +476,11 @@ size_t hq_fp4_experts_workspace_size(const hq_fp4_matrix* gate, const hq_fp4_mat
  *   y_t  = sum_j topk_w[t][j] d_{t,j}             fp32, slots ascending, rounded
  * gate, up: [n_experts * inter] rows of K = hidden, down: [n_experts * hidden]
  * rows of K = inter, each expert's rows in a run; one format; hidden and inter
- * multiples of 128, n_experts <= 1024, T <= 2^20, k <= 32
+ * multiples of 128, n_experts <= 1024, T <= 2^20, k <= 32, T*k <= 2^23
  * (HQ_ERR_UNSUPPORTED otherwise).  tensor_scale: one value, or one per expert.
+ * Nothing is rotated here: x may come out of hq_rotate with gate and up packed
+ * in the same basis, h is packed as it is and takes a down matrix in the plain
+ * basis (hq_moe_experts rotates both).
  * x: [T][hidden], row stride ldx, as in hq_fp4_quantize; x_scale, h_scale:
  * tensor scales of the two quantisations (NV; NULL: 1).  Ids outside [0,
  * n_experts) add nothing (a token without a valid id gets zeros).  y:
