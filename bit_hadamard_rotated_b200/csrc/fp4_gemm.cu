@@ -229,22 +229,24 @@ struct Item {
   int c0, c1;  // chunks of K
 };
 
-// A CTA's items.  Expert tiles count token tiles fastest.  The gated product
-// deals them out one by one, so that the CTAs that take a weight tile's other
-// uses, and an expert's tokens' other uses, run at the same time and find them
-// in L2: with an even run of tiles per CTA, whose second use of a weight tile
-// comes 6 us after the first, it read 427 MB for 340, and the layer took 254 us
-// at 4096 tokens, 237 so.  The second product keeps its runs: its tiles have
-// few chunks, and the next tile of a run is found sooner (32 tokens 51.0 us,
-// dealt out 51.7; at 4096 tokens 237 and, dealt out, 229).
+// A CTA's items.  Expert tiles count token tiles fastest and are dealt out one
+// by one, so that the CTAs that take a weight tile's other uses, and an
+// expert's tokens' other uses, run at the same time and find them in L2: with
+// an even run of tiles per CTA, whose second use of a weight tile comes 6 us
+// after the first, the gated product read 427 MB for 340, and the layer took
+// 254 us at 4096 tokens (237 with only the second product in runs, 229 so).
+// The second product of small token tiles keeps runs: its tiles have few chunks
+// and few readers, and the next tile of a run is found sooner (32 tokens 51.0
+// us, dealt out 51.7).
 template <int NT, int MODE>
 struct Walk {
+  static constexpr bool kDealt = MODE == kGated || (MODE == kGrouped && NT > 64);
   int u, end;
   const int* first;  // groups: [E + 1] tiles before each expert, then [E] segment starts, [E] row counts
-  int e, ni, mi;     // groups: the next tile (gated: an expert at or before its own)
+  int e, ni, mi;     // groups: the next tile (dealt out: an expert at or before its own)
   int rows, start;   // groups: of expert e
   __device__ __forceinline__ Walk(const GemmArgs& a, const int* groups) : first(groups) {
-    if constexpr (MODE == kGated) {
+    if constexpr (kDealt) {
       u = blockIdx.x;
       end = uniform(first[a.E]);
       e = 0;
@@ -284,7 +286,7 @@ struct Walk {
     it.c0 = 0;
     it.c1 = a.C;
     if constexpr (MODE == kGated || MODE == kGrouped) {
-      if constexpr (MODE == kGated) {
+      if constexpr (kDealt) {
         find(a);
         u += gridDim.x;
       } else {
