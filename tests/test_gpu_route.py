@@ -331,3 +331,35 @@ def test_plans_hold_every_routing():
         assert int(plan.pos.max()) < plan.n_rows
     full = hq_moe_sort(torch.arange(128, dtype=torch.int32, device="cuda").view(16, 8), 128, align=128)
     assert int(full.offsets[-1]) == full.n_rows == 128 * 128
+
+
+def test_a_recorded_step_is_captured_and_replayed():
+    """Forward and backward in one graph (warmed up on a side stream, whose autograd graph is gone before the capture),
+    replayed with other values and another routing of the same sizes."""
+    T, k, E, H = 30, 3, 6, 40
+    x, w, f = (rnd(s, torch.float32, i).cuda().requires_grad_() for i, s in enumerate([(T, H), (T, k), (T * k, H)]))
+    ids = torch.from_numpy(routing(T, k, E, 1, 0.2)).cuda()
+    dy = rnd((T, H), torch.float32, 5).cuda()
+
+    def step():
+        plan = hq_moe_sort(ids, E)
+        y = hq_moe_combine(hq_moe_gather(x, plan) * f, plan, w)
+        return (y.detach(), *torch.autograd.grad(y, (x, w, f), dy))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for seed in range(3):
+        with torch.no_grad():
+            x.copy_(rnd((T, H), torch.float32, 10 + seed))
+            w.copy_(rnd((T, k), torch.float32, 20 + seed))
+        ids.copy_(torch.from_numpy(routing(T, k, E, 30 + seed, 0.3 * seed)))
+        g.replay()
+        have = [t.clone() for t in got]
+        assert all(torch.equal(a, b) for a, b in zip(have, step()))
